@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackP
 // One block per slot: copy all bytes, then publish the table entry.
 __global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ CopyParams p) {
   const CopyDesc d = p.desc[blockIdx.x];
-  const int64_t bytes = d.fmt == 0 ? p.fp8_slot_bytes : p.tq3_slot_bytes;
-  uint8_t* slab = d.fmt == 0 ? p.fp8_slab : p.tq3_slab;
+  const int64_t bytes = d.fmt == 1 ? p.tq3_slot_bytes : p.fp8_slot_bytes;  // BF16 pages: first slab
+  uint8_t* slab = d.fmt == 1 ? p.tq3_slab : p.fp8_slab;
   const uint4* s = reinterpret_cast<const uint4*>(slab + d.src_slot * bytes);
   uint4* t = reinterpret_cast<uint4*>(slab + d.dst_slot * bytes);
   for (int64_t i = threadIdx.x; i < bytes / 16; i += blockDim.x) t[i] = s[i];
