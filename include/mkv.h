@@ -310,6 +310,27 @@ MKV_API int mkv_prefill_kv(mkv_pool_t pool, const int32_t* seq_ids, const int32_
                            int32_t n_seqs, const void* k_bf16, const void* v_bf16,
                            int32_t anchor_window_tokens, void* stream);
 
+/* Causal attention over whole prompts, for the prompt phase that precedes mkv_prefill_kv (decode
+ * attends at most 32 query columns per KV head).  n_tokens (host, n_prompts entries, each >= 0)
+ * are the lengths of prompts packed one after another without padding: prompt i takes the next
+ * n_tokens[i] rows of q, k, v and out.  For token t of a prompt and query head hq:
+ *     out[t][hq][:] = sum_{u <= t} softmax_u(sm_scale * q[t][hq] . k[u][hq / g]) v[u][hq / g]
+ * over the tokens u of the same prompt, g = num_q_heads / Hkv.  The pool gives Hkv, D and the
+ * status word; its pages are neither read nor written.
+ *   q    device bf16, rows of [num_q_heads][D], q_stride elements from row to row
+ *   k, v device bf16, rows of [Hkv][D], k_stride and v_stride elements from row to row
+ *   out  device bf16 [sum(n_tokens)][num_q_heads][D]; rows beyond are left as they were
+ * Strides are multiples of 8 elements and at least a row, pointers 16-byte aligned, out overlaps
+ * no input.  A masked key or value never reaches an output, also where it is infinite or NaN;
+ * visible ones propagate as in the formula.  Sums and the softmax are fp32; the probabilities are
+ * rounded to bf16 before they multiply v, the result once more.  Needs no workspace and keeps no
+ * state: calls may overlap on different streams and may be captured.  Errors: INVALID_ARG (also
+ * sm_scale negative or not finite), UNSUPPORTED (g > 128), CUDA. */
+MKV_API int mkv_prompt_attention(mkv_pool_t pool, const int32_t* n_tokens, int32_t n_prompts,
+                                 const void* q_bf16, int64_t q_stride, const void* k_bf16,
+                                 int64_t k_stride, const void* v_bf16, int64_t v_stride,
+                                 int32_t num_q_heads, float sm_scale, void* out_bf16, void* stream);
+
 /* Materialising profile (pt page, section "Qualidade em contexto longo": the profile in which
  * the hybrid pages really are expanded into tensors).  A debugging and quality-control path,
  * never part of decode: writes the sequence's dequantised K and V as dense fp32

@@ -23,6 +23,7 @@ ERRORS = {0: "OK", -1: "INVALID_ARG", -2: "BAD_SEQ", -3: "OUT_OF_PAGES", -4: "EM
 
 # exported symbol -> (restype, argtypes)
 _P = ctypes.c_void_p
+_I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _SZP = ctypes.POINTER(ctypes.c_size_t)
@@ -55,6 +56,8 @@ SIGNATURES = {
     "mkv_seq_copy": (ctypes.c_int, [_P, _I32, _I32, _P]),
     "mkv_materialise_kv": (ctypes.c_int, [_P, _I32, _P, _P, ctypes.c_int64, _P]),
     "mkv_prefill_kv": (ctypes.c_int, [_P, _I32P, _I32P, _I32, _P, _P, _I32, _P]),
+    "mkv_prompt_attention": (ctypes.c_int, [_P, _I32P, _I32, _P, _I64, _P, _I64, _P, _I64, _I32,
+                                            ctypes.c_float, _P, _P]),
     "mkv_selftest_wait": (ctypes.c_int, [_P, ctypes.c_int64, _P]),
     "mkv_selftest_tc_logits": (ctypes.c_int, [_P, _P, _P, _P, _P]),
     "mkv_get_block_table": (ctypes.c_int, [_P, _I32, _I32P, _I32, _I32P, _I32P]),
@@ -125,6 +128,24 @@ def _dev_ptr(t, dtype, name):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows_ptr(t, heads, dim, name, device):
+    """Pointer and row stride (elements) of a bf16 [rows, heads, dim] tensor whose rows are
+    contiguous but may be further apart, such as a part of a fused projection's output."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the pool on {device}")
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+        raise ValueError(f"{name} must be [rows, {heads}, {dim}]")
+    if t.numel() and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: each row must be contiguous")
+    stride = t.stride(0) if t.shape[0] > 1 else heads * dim
+    return ctypes.c_void_p(t.data_ptr()), stride
 
 
 class Pool:
@@ -278,6 +299,39 @@ class Pool:
         _check(lib().mkv_decode_attention(self.handle, sp, s.size, q_len, qp, Hq,
                                           ctypes.c_float(scale), op, wp, workspace.numel(),
                                           _stream_ptr(stream)), "mkv_decode_attention")
+        return out
+
+    def _stream(self, stream):
+        """The given stream, or the current one of the pool's device."""
+        import torch
+        s = stream if stream is not None else torch.cuda.current_stream(self.buffers[0].device)
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def prompt_attention(self, q, k, v, n_tokens, sm_scale=None, out=None, stream=None):
+        """Causal attention over packed prompts of ``n_tokens`` tokens each: q bf16 [rows, Hq, D],
+        k and v bf16 [rows, Hkv, D] (rows may be strided) -> bf16 [rows, Hq, D].  Rows beyond
+        sum(n_tokens) are ignored, and in a given ``out`` left as they were
+        (mkv_prompt_attention)."""
+        import torch
+        n, np_ = _i32_array(n_tokens)
+        if self.host_only:
+            raise ValueError("host-only pools have no device")
+        dev = self.buffers[0].device
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [rows, Hq, head_dim]")
+        Hq, rows = q.shape[1], int(n.astype(np.int64).clip(min=0).sum())
+        (qp, qs), (kp, ks), (vp, vs) = (_rows_ptr(t, h, self.D, name, dev) for t, h, name in
+                                        ((q, Hq, "q"), (k, self.Hkv, "k"), (v, self.Hkv, "v")))
+        if min(q.shape[0], k.shape[0], v.shape[0]) < rows:
+            raise ValueError(f"q, k and v must have the {rows} rows of n_tokens")
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        op = _dev_ptr(out, torch.bfloat16, "out")
+        if out.device != dev or out.dim() != 3 or tuple(out.shape[1:]) != (Hq, self.D) or out.shape[0] < rows:
+            raise ValueError(f"out must be [{rows} or more, {Hq}, {self.D}] on {dev}")
+        scale = 1.0 / math.sqrt(self.D) if sm_scale is None else float(sm_scale)
+        _check(lib().mkv_prompt_attention(self.handle, np_, n.size, qp, qs, kp, ks, vp, vs, Hq, scale, op,
+                                          self._stream(stream)), "mkv_prompt_attention")
         return out
 
     def reset(self, seq, stream=None):

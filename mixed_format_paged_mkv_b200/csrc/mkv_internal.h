@@ -171,10 +171,36 @@ struct DecodeParams {
   uint16_t cta_unit0[kDecodeMaxUnits + 1];  // CTA c takes units [cta_unit0[c], cta_unit0[c+1])
 };
 
+// ------------------------------------------------------------------ prompt attention
+// A unit is the query tokens of one CTA's work for one KV head; a prompt's units are consecutive.
+struct PromptSeq {
+  int32_t row0;      // first packed row
+  int32_t len;       // tokens (> 0)
+  int32_t unit_end;  // one past the prompt's last unit
+};
+constexpr int kPromptMaxSeqs = 2048;
+constexpr int kPromptMaxGroup = 128;  // query heads per KV head: a tile holds them all
+struct PromptParams {
+  uint16_t* out;      // bf16 bits [rows][Hq][D]
+  const uint16_t* v;  // for the values that cannot pass the tensor core (see prompt_attn.cu)
+  int64_t v_stride;   // elements between rows of v
+  int32_t* status;
+  float c;            // sm_scale * log2(e)
+  int32_t Hkv, Hq, g, D;
+  int32_t tile_tokens;  // tokens of a 128-row query tile
+  int32_t n_seqs, n_units;
+  PromptSeq seq[kPromptMaxSeqs];  // longest first
+};
+struct PromptInputs {
+  const void *q, *k, *v;                // bf16, rows of H heads of D
+  int64_t q_stride, k_stride, v_stride; // elements between rows
+  int64_t rows;                         // packed rows of all prompts
+};
+
 // Every parameter block fits the 32,764-byte kernel-parameter limit.
 static_assert(sizeof(AppendParams) <= 32764 && sizeof(DemoteParams) <= 32764 &&
                   sizeof(RetagParams) <= 32764 && sizeof(PackParams) <= 32764 &&
-                  sizeof(CopyParams) <= 32764 && sizeof(DecodeParams) <= 32764,
+                  sizeof(CopyParams) <= 32764 && sizeof(PromptParams) <= 32000 && sizeof(DecodeParams) <= 32764,
               "kernel parameter block too large");
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
@@ -183,6 +209,8 @@ cudaError_t launch_retag(const RetagParams& p, cudaStream_t s);
 cudaError_t launch_copy(const CopyParams& p, cudaStream_t s);
 cudaError_t launch_materialise(const MaterialiseParams& p, cudaStream_t s);
 cudaError_t launch_pack(const PackParams& p, cudaStream_t s);
+cudaError_t launch_prompt(const PromptParams& p, const PromptInputs& in, cudaStream_t s);
+int prompt_tiles_per_unit(int D);  // 128-row query tiles of a unit
 cudaError_t launch_partial(const DecodeParams& p, cudaStream_t s);
 cudaError_t launch_merge(const DecodeParams& p, cudaStream_t s);
 bool partial_supported(int D, int NC);

@@ -12,6 +12,8 @@
 #include <cstdio>
 #include <cstring>
 #include <functional>
+#include <memory>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -117,6 +119,7 @@ struct mkv_pool {
   int32_t* d_status = nullptr;
   int64_t fp8_slot_bytes = 0, tq3_slot_bytes = 0;
   int sm_count = 148;
+  int device = 0;  // device of the buffers (the current one at creation)
   int decode_sms = 0;  // SMs decode plans for (0: all of the device's)
   std::vector<Seq> seqs;
   Allocator alloc[2];
@@ -216,6 +219,18 @@ int validate_config(const mkv_pool_config* c) {
     return fail(MKV_ERR_INVALID_ARG, "max_pages_per_seq too large: token counts are int32");
   return MKV_OK;
 }
+
+// Makes the pool's device current for the calls that take tensors of their own.
+struct DeviceGuard {
+  int before = 0;
+  bool moved = false;
+  explicit DeviceGuard(int device) {
+    moved = cudaGetDevice(&before) == cudaSuccess && before != device && cudaSetDevice(device) == cudaSuccess;
+  }
+  ~DeviceGuard() {
+    if (moved) cudaSetDevice(before);
+  }
+};
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
@@ -712,6 +727,7 @@ int mkv_pool_create(const mkv_pool_config* cfg, void* fp8_slab, void* tq3_slab,
   if (!host_only) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
+    p->device = dev;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->sm_count, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
       e = cudaMemsetAsync(d_tables, 0xFF, static_cast<size_t>(cfg->max_seqs) * cfg->max_pages_per_seq * 4, 0);
@@ -1169,6 +1185,84 @@ int mkv_seq_reset(mkv_pool_t p, int32_t seq, void* stream) {
   for (int32_t e : s.table) p->alloc[slab_of(fmt_of(e))].give(slot_of(e));
   s = Seq();
   return ok();
+}
+
+int mkv_prompt_attention(mkv_pool_t p, const int32_t* n_tokens, int32_t n_prompts, const void* q_bf16,
+                         int64_t q_stride, const void* k_bf16, int64_t k_stride, const void* v_bf16,
+                         int64_t v_stride, int32_t Hq, float sm_scale, void* out_bf16, void* stream) try {
+  if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
+  if (n_prompts < 0 || (n_prompts > 0 && !n_tokens)) return fail(MKV_ERR_INVALID_ARG, "bad prompt list");
+  const int Hkv = p->cfg.num_kv_heads, D = p->cfg.head_dim;
+  if (Hq < Hkv || Hq % Hkv) return fail(MKV_ERR_INVALID_ARG, "num_q_heads %d not a multiple of Hkv %d", Hq, Hkv);
+  const int g = Hq / Hkv;
+  if (!std::isfinite(sm_scale) || sm_scale < 0)
+    return fail(MKV_ERR_INVALID_ARG, "sm_scale must be finite and not negative");
+  if (g > kPromptMaxGroup)
+    return fail(MKV_ERR_UNSUPPORTED, "num_q_heads / Hkv = %d > %d is not built", g, kPromptMaxGroup);
+  int64_t rows = 0;
+  for (int32_t i = 0; i < n_prompts; ++i) {
+    if (n_tokens[i] < 0) return fail(MKV_ERR_INVALID_ARG, "negative token count");
+    rows += n_tokens[i];
+  }
+  if (rows > INT32_MAX) return fail(MKV_ERR_INVALID_ARG, "too many tokens");
+  if (rows == 0) return ok();
+  if (!q_bf16 || !k_bf16 || !v_bf16 || !out_bf16) return fail(MKV_ERR_INVALID_ARG, "q/k/v/out is NULL");
+  struct Input { const char* name; const void* ptr; int64_t stride, width; };
+  const Input in[3] = {{"q", q_bf16, q_stride, static_cast<int64_t>(Hq) * D},
+                       {"k", k_bf16, k_stride, static_cast<int64_t>(Hkv) * D},
+                       {"v", v_bf16, v_stride, static_cast<int64_t>(Hkv) * D}};
+  const uintptr_t o0 = reinterpret_cast<uintptr_t>(out_bf16), o1 = o0 + rows * in[0].width * 2;
+  for (const Input& x : in) {
+    if (x.stride < x.width || x.stride % 8 || x.stride >= (1LL << 38))
+      return fail(MKV_ERR_INVALID_ARG, "%s: row stride %lld must be a multiple of 8 elements, at least %lld", x.name,
+                  static_cast<long long>(x.stride), static_cast<long long>(x.width));
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(x.ptr);
+    if (a0 & 15) return fail(MKV_ERR_INVALID_ARG, "%s must be 16-byte aligned", x.name);
+    if (a0 < o1 && o0 < a0 + ((rows - 1) * x.stride + x.width) * 2)
+      return fail(MKV_ERR_INVALID_ARG, "out overlaps %s", x.name);
+  }
+  if (o0 & 15) return fail(MKV_ERR_INVALID_ARG, "out must be 16-byte aligned");
+  if (p->host_only) return fail(MKV_ERR_INVALID_ARG, "host-only pool cannot attend");
+
+  // ---- the prompts, longest first (the CTAs start in this order), in launches of whole prompts
+  std::vector<PromptSeq> seqs;
+  int32_t row = 0;
+  for (int32_t i = 0; i < n_prompts; row += n_tokens[i++])
+    if (n_tokens[i] > 0) seqs.push_back({row, n_tokens[i], 0});
+  std::stable_sort(seqs.begin(), seqs.end(), [](const PromptSeq& a, const PromptSeq& b) { return a.len > b.len; });
+  const DeviceGuard guard(p->device);
+  std::unique_ptr<PromptParams> prm(new PromptParams);
+  prm->out = static_cast<uint16_t*>(out_bf16);
+  prm->v = static_cast<const uint16_t*>(v_bf16);
+  prm->v_stride = v_stride;
+  prm->status = p->d_status;
+  prm->c = sm_scale * 1.4426950408889634f;
+  prm->Hkv = Hkv;
+  prm->Hq = Hq;
+  prm->g = g;
+  prm->D = D;
+  prm->tile_tokens = 128 / g;
+  const PromptInputs inputs{q_bf16, k_bf16, v_bf16, q_stride, k_stride, v_stride, rows};
+  const int64_t unit_tokens = static_cast<int64_t>(prm->tile_tokens) * prompt_tiles_per_unit(D);
+  for (size_t b = 0; b < seqs.size();) {
+    int64_t units = 0;
+    prm->n_seqs = 0;
+    for (; b < seqs.size() && prm->n_seqs < kPromptMaxSeqs; ++b) {
+      const int64_t u = (seqs[b].len + unit_tokens - 1) / unit_tokens;
+      if ((units + u) * Hkv > INT32_MAX) break;  // CTAs of a grid
+      units += u;
+      seqs[b].unit_end = static_cast<int32_t>(units);
+      prm->seq[prm->n_seqs++] = seqs[b];
+    }
+    if (prm->n_seqs == 0) return fail(MKV_ERR_UNSUPPORTED, "a prompt of %d tokens needs too many CTAs", seqs[b].len);
+    prm->n_units = static_cast<int32_t>(units);
+    const cudaError_t e = launch_prompt(*prm, inputs, as_stream(stream));
+    ++p->launches;
+    if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
+  }
+  return ok();
+} catch (const std::bad_alloc&) {
+  return fail(MKV_ERR_INVALID_ARG, "out of host memory");
 }
 
 int mkv_selftest_wait(mkv_pool_t p, int64_t limit_ns, void* stream) {

@@ -14,8 +14,8 @@ def compare_pages(lp, op, seqs):
     for s in seqs:
         t, ctx = lp.block_table(s)
         assert t == op.block_table(s) and ctx == op.ctx[s], s
-        row = lp.buffers[2].view(torch.int32).view(lp.cfg.max_seqs, -1)[s, :lp.cfg.max_pages_per_seq]
-        row = row.cpu().numpy()
+        cols = lp.cfg.max_pages_per_seq
+        row = lp.buffers[2].view(torch.int32)[s * cols:(s + 1) * cols].cpu().numpy()
         assert row[:len(t)].tolist() == t, s
         for p, e in enumerate(t):
             assert np.array_equal(lp.read_slot(e), op.slot_bytes(e)), f"seq {s} page {p} {e:#x}"
