@@ -266,6 +266,41 @@ MKV_API int mkv_seq_reset(mkv_pool_t pool, int32_t seq, void* stream);
  * OUT_OF_PAGES (nothing changed), CUDA. */
 MKV_API int mkv_seq_copy(mkv_pool_t pool, int32_t src, int32_t dst, void* stream);
 
+/* Branch sequences (parallel sampling, beams, a cached prompt prefix): each empty sequence
+ * dst_ids[i] gets the first n_tokens[i] tokens of src_ids[i] (n_tokens NULL: all of them).  Full
+ * pages are shared, not copied: both sequences' tables name the same slot, which is free again
+ * when its last holder gives it up.  A partial last page is copied into an FP8 (BF16) slot of the
+ * branch's own, its rows past n_tokens[i] zero, its scales kept; so appends never write a shared
+ * page.  Protection flags are copied.  Sources may repeat; destinations are distinct and not among
+ * the sources.  A branch lives on as any sequence: demoting a page that others keep as FP8 gives
+ * the listed sequences one TQ3 page and leaves theirs.  Slots taken lowest-order-first in list
+ * order.  Errors: BAD_SEQ, INVALID_ARG, UNSUPPORTED (n_tokens[i] ends inside a TQ3 page),
+ * OUT_OF_PAGES (nothing changed), CUDA. */
+MKV_API int mkv_seq_fork(mkv_pool_t pool, const int32_t* src_ids, const int32_t* dst_ids,
+                         const int32_t* n_tokens, int32_t n_forks, void* stream);
+
+/* Roll sequences back to their first n_tokens[i] tokens (rejected speculative tokens): pages past
+ * the new end are given up, rows past it in its page become zero (the page's scales stay), after
+ * the page was copied to a slot of the sequence's own where others share it.  Slots are taken in
+ * list order before any is freed.  A call split over several launches (more than 960 sequences)
+ * takes effect launch by launch in list order, so one that fails has rolled back a leading part
+ * of the list.  Errors: BAD_SEQ, INVALID_ARG (also n_tokens[i] above the length), UNSUPPORTED
+ * (n_tokens[i] ends inside a TQ3 page), OUT_OF_PAGES (nothing changed), CUDA. */
+MKV_API int mkv_seq_truncate(mkv_pool_t pool, const int32_t* seq_ids, const int32_t* n_tokens,
+                             int32_t n_seqs, void* stream);
+
+/* mkv_seq_reset for a list of distinct sequences, in one launch (per 960 sequences; a call split
+ * over several takes effect launch by launch). */
+MKV_API int mkv_seq_free(mkv_pool_t pool, const int32_t* seq_ids, int32_t n_seqs, void* stream);
+
+/* Close the holes that freed pages left: in each slab every held slot that is not among the first
+ * `held` slots of the slot order moves to a free slot among them (both in order), and the tables
+ * follow.  Afterwards the slots in use are the first ones of the order (their counts: see
+ * mkv_pool_stats), so a cache can be saved or moved as one range per slab.  *n_moved (may be NULL)
+ * receives the pages moved.  A call split over several launches (more than 1200 pages of a
+ * format) takes effect launch by launch.  Errors: INVALID_ARG, CUDA. */
+MKV_API int mkv_pool_compact(mkv_pool_t pool, int32_t* n_moved, void* stream);
+
 /* Host copy of a sequence's block table: up to cap entries into host_out (may be NULL when
  * cap == 0); *n_pages and *ctx_len (may be NULL) receive the page count and length. */
 MKV_API int mkv_get_block_table(mkv_pool_t pool, int32_t seq, int32_t* host_out, int32_t cap,
@@ -343,7 +378,7 @@ MKV_API int mkv_materialise_kv(mkv_pool_t pool, int32_t seq, float* k_out, float
                                int64_t max_tokens, void* stream);
 
 /* Footprint (section "Memória e compressão"): live tokens, pages per format and KV slab bytes
- * held by live pages per live token. */
+ * held by live pages per live token.  A page that sequences share counts once. */
 MKV_API int mkv_pool_stats(mkv_pool_t pool, int64_t* live_tokens, int32_t* fp8_pages,
                            int32_t* tq3_pages, double* kv_bytes_per_token);
 

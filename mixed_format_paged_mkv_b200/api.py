@@ -54,6 +54,10 @@ SIGNATURES = {
                                                     ctypes.c_float, _P, _P]),
     "mkv_seq_reset": (ctypes.c_int, [_P, _I32, _P]),
     "mkv_seq_copy": (ctypes.c_int, [_P, _I32, _I32, _P]),
+    "mkv_seq_fork": (ctypes.c_int, [_P, _I32P, _I32P, _I32P, _I32, _P]),
+    "mkv_seq_truncate": (ctypes.c_int, [_P, _I32P, _I32P, _I32, _P]),
+    "mkv_seq_free": (ctypes.c_int, [_P, _I32P, _I32, _P]),
+    "mkv_pool_compact": (ctypes.c_int, [_P, _I32P, _P]),
     "mkv_materialise_kv": (ctypes.c_int, [_P, _I32, _P, _P, ctypes.c_int64, _P]),
     "mkv_prefill_kv": (ctypes.c_int, [_P, _I32P, _I32P, _I32, _P, _P, _I32, _P]),
     "mkv_prompt_attention": (ctypes.c_int, [_P, _I32P, _I32, _P, _I64, _P, _I64, _P, _I64, _I32,
@@ -341,6 +345,40 @@ class Pool:
     def copy(self, src, dst, stream=None):
         st = None if self.host_only else _stream_ptr(stream)
         _check(lib().mkv_seq_copy(self.handle, src, dst, st), "mkv_seq_copy")
+
+    def fork(self, src_ids, dst_ids, n_tokens=None, stream=None):
+        """Give each empty sequence of ``dst_ids`` the first tokens (default: all) of its source,
+        sharing full pages copy-on-write (mkv_seq_fork)."""
+        s, sp = _i32_array(src_ids)
+        d, dp = _i32_array(dst_ids)
+        n, np_ = (None, None) if n_tokens is None else _i32_array(n_tokens)
+        if d.size != s.size or (n is not None and n.size != s.size):
+            raise ValueError("src_ids, dst_ids and n_tokens must have the same length")
+        st = None if self.host_only else self._stream(stream)
+        _check(lib().mkv_seq_fork(self.handle, sp, dp, np_, s.size, st), "mkv_seq_fork")
+
+    def truncate(self, seq_ids, n_tokens, stream=None):
+        """Roll sequences back to their first ``n_tokens`` tokens (mkv_seq_truncate)."""
+        s, sp = _i32_array(seq_ids)
+        n, np_ = _i32_array(n_tokens)
+        if n.size != s.size:
+            raise ValueError("seq_ids and n_tokens must have the same length")
+        st = None if self.host_only else self._stream(stream)
+        _check(lib().mkv_seq_truncate(self.handle, sp, np_, s.size, st), "mkv_seq_truncate")
+
+    def free(self, seq_ids, stream=None):
+        """Free every page of several sequences (mkv_seq_free)."""
+        s, sp = _i32_array(seq_ids)
+        st = None if self.host_only else self._stream(stream)
+        _check(lib().mkv_seq_free(self.handle, sp, s.size, st), "mkv_seq_free")
+
+    def compact(self, stream=None):
+        """Move pages so that the slots in use are the first ones of each slab's order; returns
+        the number of pages moved (mkv_pool_compact)."""
+        n = ctypes.c_int32(0)
+        st = None if self.host_only else self._stream(stream)
+        _check(lib().mkv_pool_compact(self.handle, ctypes.byref(n), st), "mkv_pool_compact")
+        return n.value
 
     def materialise(self, seq, k_out=None, v_out=None, stream=None):
         """Dense fp32 dequantised K and V of a sequence, [ctx, Hkv, D] each (a debugging and

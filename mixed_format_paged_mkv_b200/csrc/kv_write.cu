@@ -350,19 +350,6 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackP
     p.tables[d.table_index] = static_cast<int32_t>((1u << kFmtShift) | static_cast<uint32_t>(d.dst_slot));
 }
 
-// One block per slot: copy all bytes, then publish the table entry.
-__global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ CopyParams p) {
-  const CopyDesc d = p.desc[blockIdx.x];
-  const int64_t bytes = d.fmt == 1 ? p.tq3_slot_bytes : p.fp8_slot_bytes;  // BF16 pages: first slab
-  uint8_t* slab = d.fmt == 1 ? p.tq3_slab : p.fp8_slab;
-  const uint4* s = reinterpret_cast<const uint4*>(slab + d.src_slot * bytes);
-  uint4* t = reinterpret_cast<uint4*>(slab + d.dst_slot * bytes);
-  for (int64_t i = threadIdx.x; i < bytes / 16; i += blockDim.x) t[i] = s[i];
-  if (threadIdx.x == 0)
-    p.tables[d.table_index] =
-        static_cast<int32_t>((static_cast<uint32_t>(d.fmt) << kFmtShift) | static_cast<uint32_t>(d.dst_slot));
-}
-
 // Materialising profile ("Minima-KV ..." pt page, section "Qualidade em contexto longo": the
 // profile in which the hybrid pages really are expanded into tensors).  A debugging and
 // quality-control path: one CTA per (page, KV head, K/V) writes the page's dequantised values
@@ -453,12 +440,6 @@ cudaError_t launch_demote(const DemoteParams& p, cudaStream_t s) {
 cudaError_t launch_retag(const RetagParams& p, cudaStream_t s) {
   if (p.n <= 0) return cudaSuccess;
   retag_kernel<<<(p.n + 255) / 256, 256, 0, s>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_copy(const CopyParams& p, cudaStream_t s) {
-  if (p.n_desc <= 0) return cudaSuccess;
-  copy_kernel<<<p.n_desc, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 

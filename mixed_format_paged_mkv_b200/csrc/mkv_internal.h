@@ -93,18 +93,31 @@ struct PackParams {
   PackDesc desc[kPackMaxDesc];
 };
 
-// ------------------------------------------------------------------ slot copy
-struct CopyDesc {
-  int32_t src_slot, dst_slot, fmt, table_index;
+// ------------------------------------------------------------------ page operations
+struct PageMove {
+  int32_t src_slot, dst_slot;  // equal: the page is cut where it is
+  int32_t table_index;  // entry that gets the new slot; of a shared page its table column
+  uint8_t fmt;
+  uint8_t kept;         // token rows kept; the others become zero (16: all kept)
+  uint8_t shared;       // 1: every entry of the column that names the old slot gets the new one
+  uint8_t pad;
 };
-constexpr int kCopyMaxDesc = 1920;
-struct CopyParams {
+struct RowMove {
+  int32_t src;    // first table index read, -1: the entries become unmapped
+  int32_t dst;    // first table index written
+  int32_t count;
+};
+constexpr int kPageMoveMax = 1200, kRowMoveMax = 960;
+struct PageOpParams {
   uint8_t* fp8_slab;
   uint8_t* tq3_slab;
   int32_t* tables;
   int64_t fp8_slot_bytes, tq3_slot_bytes;
-  int32_t n_desc;
-  CopyDesc desc[kCopyMaxDesc];
+  int32_t D, max_seqs, max_pages;
+  int32_t pieces;  // CTAs per page (set by the launcher)
+  int32_t n_page, n_row;
+  PageMove page[kPageMoveMax];
+  RowMove row[kRowMoveMax];
 };
 
 // ------------------------------------------------------------------ materialise (debug / QC)
@@ -200,13 +213,13 @@ struct PromptInputs {
 // Every parameter block fits the 32,764-byte kernel-parameter limit.
 static_assert(sizeof(AppendParams) <= 32764 && sizeof(DemoteParams) <= 32764 &&
                   sizeof(RetagParams) <= 32764 && sizeof(PackParams) <= 32764 &&
-                  sizeof(CopyParams) <= 32764 && sizeof(PromptParams) <= 32000 && sizeof(DecodeParams) <= 32764,
+                  sizeof(PageOpParams) <= 32764 && sizeof(PromptParams) <= 32000 && sizeof(DecodeParams) <= 32764,
               "kernel parameter block too large");
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_demote(const DemoteParams& p, cudaStream_t s);
 cudaError_t launch_retag(const RetagParams& p, cudaStream_t s);
-cudaError_t launch_copy(const CopyParams& p, cudaStream_t s);
+cudaError_t launch_page_ops(PageOpParams& p, cudaStream_t s);
 cudaError_t launch_materialise(const MaterialiseParams& p, cudaStream_t s);
 cudaError_t launch_pack(const PackParams& p, cudaStream_t s);
 cudaError_t launch_prompt(const PromptParams& p, const PromptInputs& in, cudaStream_t s);

@@ -15,6 +15,7 @@
 #include <memory>
 #include <new>
 #include <string>
+#include <unordered_map>
 #include <vector>
 
 #include "mkv.h"
@@ -46,10 +47,12 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(MKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// Free slots handed out lowest rank first; rank = position in the slot order.
+// Free slots handed out lowest rank first; rank = position in the slot order.  A slot that several
+// sequences share is free again when the last of them gives it back.
 struct Allocator {
   int32_t n = 0;
   std::vector<int32_t> rank;
+  std::vector<int32_t> refs;   // sequences that hold the slot
   std::vector<uint8_t> is_free;
   std::vector<uint64_t> heap;  // (rank << 32) | slot, min-heap
   int32_t n_free = 0;
@@ -57,6 +60,7 @@ struct Allocator {
   void init(int32_t slots) {
     n = slots;
     rank.resize(n);
+    refs.assign(n, 0);
     is_free.assign(n, 1);
     for (int32_t i = 0; i < n; ++i) rank[i] = i;
     rebuild();
@@ -76,10 +80,12 @@ struct Allocator {
     const int32_t s = static_cast<int32_t>(heap.back() & 0xffffffffu);
     heap.pop_back();
     is_free[s] = 0;
+    refs[s] = 1;
     --n_free;
     return s;
   }
   void give(int32_t s) {
+    if (--refs[s] > 0) return;
     is_free[s] = 1;
     ++n_free;
     heap.push_back((static_cast<uint64_t>(rank[s]) << 32) | static_cast<uint32_t>(s));
@@ -667,6 +673,46 @@ int device_op(mkv_pool_t p, const char* what, F&& f) {
   return e == cudaSuccess ? MKV_OK : cuda_fail(e, what);
 }
 
+// Page moves and table runs of a call, issued as one launch when a list is full or at the end.
+struct PageOps {
+  mkv_pool_t p;
+  const char* what;
+  void* stream;
+  std::unique_ptr<PageOpParams> prm{new PageOpParams};
+  PageOps(mkv_pool_t pool, const char* name, void* st) : p(pool), what(name), stream(st) {
+    prm->fp8_slab = p->fp8_slab;
+    prm->tq3_slab = p->tq3_slab;
+    prm->tables = p->d_tables;
+    prm->fp8_slot_bytes = p->fp8_slot_bytes;
+    prm->tq3_slot_bytes = p->tq3_slot_bytes;
+    prm->D = p->cfg.head_dim;
+    prm->max_seqs = p->cfg.max_seqs;
+    prm->max_pages = p->cfg.max_pages_per_seq;
+    prm->n_page = prm->n_row = 0;
+  }
+  bool fits(int pages, int rows) const {
+    return prm->n_page + pages <= kPageMoveMax && prm->n_row + rows <= kRowMoveMax;
+  }
+  int page(const PageMove& m) {
+    if (!fits(1, 0))
+      if (int e = flush()) return e;
+    prm->page[prm->n_page++] = m;
+    return MKV_OK;
+  }
+  int row(const RowMove& m) {
+    if (!fits(0, 1))
+      if (int e = flush()) return e;
+    prm->row[prm->n_row++] = m;
+    return MKV_OK;
+  }
+  int flush() {
+    if (prm->n_page + prm->n_row == 0) return MKV_OK;
+    const int rc = device_op(p, what, [&] { return launch_page_ops(*prm, as_stream(stream)); });
+    prm->n_page = prm->n_row = 0;
+    return rc;
+  }
+};
+
 cudaEvent_t get_event(mkv_pool_t p) {
   if (!p->spare_events.empty()) {
     cudaEvent_t e = p->spare_events.back();
@@ -885,22 +931,34 @@ int mkv_demote_pages(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32
       if (full && !anchor) work.push_back({seq_ids[i], pg});
     }
   }
-  if (static_cast<int64_t>(work.size()) > p->alloc[1].n_free)
-    return fail(MKV_ERR_OUT_OF_PAGES, "TQ3 slab has %d free slots, %zu needed", p->alloc[1].n_free, work.size());
-  // ---- stage: a TQ3 slot per page, in (sequence, page) order
+  // ---- stage: a TQ3 slot per page, in (sequence, page) order; a page that listed sequences
+  // share is converted once for all of them (a sharer that keeps it goes on with the FP8 page)
   std::vector<DemoteDesc> descs;
+  std::vector<int32_t> to(work.size());          // descriptor of each page of the list
+  std::unordered_map<int32_t, int32_t> shared;   // FP8 slot -> descriptor
   descs.reserve(work.size());
-  for (const Work& w : work) {
-    const Seq& s = p->seqs[w.seq];
-    descs.push_back({slot_of(s.table[w.page]), p->alloc[1].take(),
-                     w.seq * p->cfg.max_pages_per_seq + w.page});
+  for (size_t k = 0; k < work.size(); ++k) {
+    const int32_t src = slot_of(p->seqs[work[k].seq].table[work[k].page]);
+    to[k] = static_cast<int32_t>(descs.size());
+    if (p->alloc[0].refs[src] > 1) {
+      const auto at = shared.emplace(src, to[k]);
+      if (!at.second) {
+        to[k] = at.first->second;
+        continue;
+      }
+    }
+    descs.push_back({src, -1, work[k].seq * p->cfg.max_pages_per_seq + work[k].page});
   }
+  if (static_cast<int64_t>(descs.size()) > p->alloc[1].n_free)
+    return fail(MKV_ERR_OUT_OF_PAGES, "TQ3 slab has %d free slots, %zu needed", p->alloc[1].n_free, descs.size());
+  for (DemoteDesc& d : descs) d.dst_slot = p->alloc[1].take();
   // ---- launch: one launch writes the pages and publishes their table entries; a call that
   // needs several launches publishes no entry until every page is written (retag launches
   // last), so a failed launch never leaves a device entry naming an unwritten page
   int rc = MKV_OK;
   if (!descs.empty()) {
-    const bool single = descs.size() <= static_cast<size_t>(kDemoteMaxDesc);
+    // (an entry per listed page: more entries than pages where sequences share one)
+    const bool single = descs.size() <= static_cast<size_t>(kDemoteMaxDesc) && descs.size() == work.size();
     DemoteParams* prm = new DemoteParams;
     prm->fp8_slab = p->fp8_slab;
     prm->tq3_slab = p->tq3_slab;
@@ -920,12 +978,12 @@ int mkv_demote_pages(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32
     if (!single && rc == MKV_OK) {
       RetagParams* rp = new RetagParams;
       rp->tables = p->d_tables;
-      for (size_t b = 0; b < descs.size() && rc == MKV_OK; b += kRetagMax) {
-        const size_t m = std::min<size_t>(kRetagMax, descs.size() - b);
+      for (size_t b = 0; b < work.size() && rc == MKV_OK; b += kRetagMax) {
+        const size_t m = std::min<size_t>(kRetagMax, work.size() - b);
         rp->n = static_cast<int32_t>(m);
         for (size_t k = 0; k < m; ++k) {
-          rp->index[k] = descs[b + k].table_index;
-          rp->entry[k] = entry_of(MKV_FMT_TQ3, descs[b + k].dst_slot);
+          rp->index[k] = work[b + k].seq * p->cfg.max_pages_per_seq + work[b + k].page;
+          rp->entry[k] = entry_of(MKV_FMT_TQ3, descs[to[b + k]].dst_slot);
         }
         rc = device_op(p, "retag launch", [&] { return launch_retag(*rp, as_stream(stream)); });
       }
@@ -937,9 +995,11 @@ int mkv_demote_pages(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32
     return rc;
   }
   // ---- commit: retag, then free the FP8 slots (reusable by later calls in stream order)
+  for (const DemoteDesc& d : descs) p->alloc[1].refs[d.dst_slot] = 0;
   for (size_t k = 0; k < work.size(); ++k) {
     Seq& s = p->seqs[work[k].seq];
-    s.table[work[k].page] = entry_of(MKV_FMT_TQ3, descs[k].dst_slot);
+    s.table[work[k].page] = entry_of(MKV_FMT_TQ3, descs[to[k]].dst_slot);
+    p->alloc[1].refs[descs[to[k]].dst_slot] += 1;
     s.n3 += 1;
   }
   for (int32_t i = 0; i < n_seqs; ++i) {
@@ -948,8 +1008,8 @@ int mkv_demote_pages(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32
                                      [&](int32_t pg) { return fmt_of(s.table[pg]) != p->page_fmt; }),
                       s.fp8_pages.end());
   }
-  for (const DemoteDesc& d : descs) p->alloc[0].give(d.src_slot);
-  if (n_demoted) *n_demoted = static_cast<int32_t>(descs.size());
+  for (int32_t k : to) p->alloc[0].give(descs[k].src_slot);
+  if (n_demoted) *n_demoted = static_cast<int32_t>(work.size());
   return ok();
 }
 
@@ -1463,37 +1523,266 @@ int mkv_seq_copy(mkv_pool_t p, int32_t src, int32_t dst, void* stream) {
   d.prot = s.prot;
   d.n3 = s.n3;
   d.fp8_pages = s.fp8_pages;
-  std::vector<CopyDesc> descs;
+  PageOps ops(p, "copy launch", stream);
   for (size_t pg = 0; pg < s.table.size(); ++pg) {
     const int f = fmt_of(s.table[pg]);
     const int32_t ns = p->alloc[slab_of(f)].take();
     d.table.push_back(entry_of(f, ns));
-    descs.push_back({slot_of(s.table[pg]), ns, f, dst * p->cfg.max_pages_per_seq + static_cast<int32_t>(pg)});
   }
   // ---- launch (the destination was empty: entries published before a failure are ignored)
   int rc = MKV_OK;
-  if (!descs.empty()) {
-    CopyParams* prm = new CopyParams;
-    prm->fp8_slab = p->fp8_slab;
-    prm->tq3_slab = p->tq3_slab;
-    prm->tables = p->d_tables;
-    prm->fp8_slot_bytes = p->fp8_slot_bytes;
-    prm->tq3_slot_bytes = p->tq3_slot_bytes;
-    for (size_t b = 0; b < descs.size() && rc == MKV_OK; b += kCopyMaxDesc) {
-      const size_t m = std::min<size_t>(kCopyMaxDesc, descs.size() - b);
-      prm->n_desc = static_cast<int32_t>(m);
-      std::memcpy(prm->desc, descs.data() + b, m * sizeof(CopyDesc));
-      rc = device_op(p, "copy launch", [&] { return launch_copy(*prm, as_stream(stream)); });
-    }
-    delete prm;
-  }
+  for (size_t pg = 0; pg < s.table.size() && rc == MKV_OK; ++pg)
+    rc = ops.page({slot_of(s.table[pg]), slot_of(d.table[pg]),
+                   dst * p->cfg.max_pages_per_seq + static_cast<int32_t>(pg),
+                   static_cast<uint8_t>(fmt_of(s.table[pg])), kPageTokens, 0, 0});
+  if (rc == MKV_OK) rc = ops.flush();
   if (rc != MKV_OK) {
-    for (auto it = descs.rbegin(); it != descs.rend(); ++it)
-      p->alloc[slab_of(it->fmt)].give(it->dst_slot);
+    for (auto it = d.table.rbegin(); it != d.table.rend(); ++it)
+      p->alloc[slab_of(fmt_of(*it))].give(slot_of(*it));
     return rc;
   }
   p->seqs[dst] = std::move(d);
   return ok();
+}
+
+int mkv_seq_fork(mkv_pool_t p, const int32_t* src_ids, const int32_t* dst_ids, const int32_t* n_tokens,
+                 int32_t n_forks, void* stream) {
+  if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
+  if (n_forks < 0 || (n_forks > 0 && (!src_ids || !dst_ids)))
+    return fail(MKV_ERR_INVALID_ARG, "bad sequence list");
+  for (int32_t i = 0; i < n_forks; ++i)
+    if (int e = check_seq(p, src_ids[i])) return e;
+  if (int e = check_seq_list(p, dst_ids, n_forks, nullptr)) return e;
+  std::vector<uint8_t> is_src(p->cfg.max_seqs, 0);
+  for (int32_t i = 0; i < n_forks; ++i) is_src[src_ids[i]] = 1;
+  const int32_t MP = p->cfg.max_pages_per_seq;
+  int64_t need = 0;
+  for (int32_t i = 0; i < n_forks; ++i) {
+    const Seq &s = p->seqs[src_ids[i]], &d = p->seqs[dst_ids[i]];
+    if (is_src[dst_ids[i]] || !d.table.empty() || d.ctx)
+      return fail(MKV_ERR_INVALID_ARG, "fork needs an empty destination that is no source (%d is not)", dst_ids[i]);
+    const int32_t at = n_tokens ? n_tokens[i] : s.ctx;
+    if (at < 0 || at > s.ctx)
+      return fail(MKV_ERR_INVALID_ARG, "fork of sequence %d at %d tokens of %d", src_ids[i], at, s.ctx);
+    if (at % kPageTokens && fmt_of(s.table[at / kPageTokens]) == MKV_FMT_TQ3)
+      return fail(MKV_ERR_UNSUPPORTED, "%d tokens end inside a TQ3 page of sequence %d", at, src_ids[i]);
+    need += at % kPageTokens ? 1 : 0;
+  }
+  if (need > p->alloc[0].n_free)
+    return fail(MKV_ERR_OUT_OF_PAGES, "slab 0 has %d free slots, %lld needed", p->alloc[0].n_free,
+                static_cast<long long>(need));
+  // ---- stage and launch: the shared pages' entries are copied on the device, a partial last page
+  // gets a slot of its own (only full pages are ever shared, so appends never write a shared page)
+  std::vector<int32_t> taken;
+  PageOps ops(p, "fork launch", stream);
+  int rc = MKV_OK;
+  for (int32_t i = 0; i < n_forks && rc == MKV_OK; ++i) {
+    const Seq& s = p->seqs[src_ids[i]];
+    const int32_t at = n_tokens ? n_tokens[i] : s.ctx, full = at / kPageTokens;
+    if (full > 0) rc = ops.row({src_ids[i] * MP, dst_ids[i] * MP, full});
+    if (rc == MKV_OK && at % kPageTokens) {
+      taken.push_back(p->alloc[0].take());
+      rc = ops.page({slot_of(s.table[full]), taken.back(), dst_ids[i] * MP + full,
+                     static_cast<uint8_t>(p->page_fmt), static_cast<uint8_t>(at % kPageTokens), 0, 0});
+    }
+  }
+  if (rc == MKV_OK) rc = ops.flush();
+  if (rc != MKV_OK) {  // (entries published before a failure lie in empty sequences' rows: ignored)
+    for (auto it = taken.rbegin(); it != taken.rend(); ++it) p->alloc[0].give(*it);
+    return rc;
+  }
+  // ---- commit
+  size_t next = 0;
+  for (int32_t i = 0; i < n_forks; ++i) {
+    const Seq& s = p->seqs[src_ids[i]];
+    Seq& d = p->seqs[dst_ids[i]];
+    const int32_t at = n_tokens ? n_tokens[i] : s.ctx, full = at / kPageTokens;
+    const int32_t pages = (at + kPageTokens - 1) / kPageTokens;
+    d.ctx = at;
+    d.table.assign(s.table.begin(), s.table.begin() + full);
+    d.prot.assign(s.prot.begin(), s.prot.begin() + pages);
+    const auto end8 = std::lower_bound(s.fp8_pages.begin(), s.fp8_pages.end(), full);
+    d.fp8_pages.assign(s.fp8_pages.begin(), end8);
+    d.n3 = full - static_cast<int32_t>(d.fp8_pages.size());
+    for (int32_t e : d.table) ++p->alloc[slab_of(fmt_of(e))].refs[slot_of(e)];
+    if (pages > full) {
+      d.table.push_back(entry_of(p->page_fmt, taken[next++]));
+      d.fp8_pages.push_back(full);
+    }
+  }
+  return ok();
+}
+
+int mkv_seq_truncate(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_tokens, int32_t n_seqs,
+                     void* stream) {
+  if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
+  if (n_seqs < 0 || (n_seqs > 0 && (!seq_ids || !n_tokens)))
+    return fail(MKV_ERR_INVALID_ARG, "bad sequence list");
+  if (int e = check_seq_list(p, seq_ids, n_seqs, n_tokens)) return e;
+  const int32_t MP = p->cfg.max_pages_per_seq;
+  // the page that a sequence's new end lies in, -1: none; it is copied when others share it
+  auto cut_page = [&](int32_t i) {
+    const Seq& s = p->seqs[seq_ids[i]];
+    return n_tokens[i] < s.ctx && n_tokens[i] % kPageTokens ? n_tokens[i] / kPageTokens : -1;
+  };
+  int64_t need = 0;
+  for (int32_t i = 0; i < n_seqs; ++i) {
+    const Seq& s = p->seqs[seq_ids[i]];
+    if (n_tokens[i] > s.ctx)
+      return fail(MKV_ERR_INVALID_ARG, "sequence %d has %d tokens < %d", seq_ids[i], s.ctx, n_tokens[i]);
+    const int32_t pg = cut_page(i);
+    if (pg < 0) continue;
+    if (fmt_of(s.table[pg]) == MKV_FMT_TQ3)
+      return fail(MKV_ERR_UNSUPPORTED, "%d tokens end inside a TQ3 page of sequence %d", n_tokens[i], seq_ids[i]);
+    need += p->alloc[0].refs[slot_of(s.table[pg])] > 1 ? 1 : 0;
+  }
+  if (need > p->alloc[0].n_free)
+    return fail(MKV_ERR_OUT_OF_PAGES, "slab 0 has %d free slots, %lld needed", p->alloc[0].n_free,
+                static_cast<long long>(need));
+  // ---- stage and launch
+  struct Cut { int32_t i, old_slot, new_slot; };  // (old == new: the page is the sequence's own)
+  std::vector<Cut> cuts;
+  PageOps ops(p, "truncate launch", stream);
+  // commit of the sequences [a, b) of the list, whose launches were issued
+  size_t next = 0;
+  std::vector<int32_t> dropped;
+  auto commit = [&](int32_t a, int32_t b) {
+    for (int32_t i = a; i < b; ++i) {
+      Seq& s = p->seqs[seq_ids[i]];
+      if (n_tokens[i] == s.ctx) continue;
+      const int32_t keep = (n_tokens[i] + kPageTokens - 1) / kPageTokens;
+      if (next < cuts.size() && cuts[next].i == i) {
+        const Cut& c = cuts[next++];
+        if (c.new_slot != c.old_slot) {
+          dropped.push_back(s.table[keep - 1]);
+          s.table[keep - 1] = entry_of(p->page_fmt, c.new_slot);
+        }
+      }
+      dropped.insert(dropped.end(), s.table.begin() + keep, s.table.end());
+      s.table.resize(keep);
+      s.prot.resize(keep);
+      s.fp8_pages.erase(std::lower_bound(s.fp8_pages.begin(), s.fp8_pages.end(), keep), s.fp8_pages.end());
+      s.n3 = keep - static_cast<int32_t>(s.fp8_pages.size());
+      s.ctx = n_tokens[i];
+    }
+  };
+  int rc = MKV_OK;
+  int32_t done = 0;
+  for (int32_t i = 0; i < n_seqs && rc == MKV_OK; ++i) {
+    if (!ops.fits(1, 1)) {
+      if ((rc = ops.flush()) != MKV_OK) break;
+      commit(done, i);
+      done = i;
+    }
+    const Seq& s = p->seqs[seq_ids[i]];
+    const int32_t keep = (n_tokens[i] + kPageTokens - 1) / kPageTokens;
+    const int32_t pages = static_cast<int32_t>(s.table.size()), pg = cut_page(i);
+    if (pages > keep) ops.row({-1, seq_ids[i] * MP + keep, pages - keep});
+    if (pg >= 0) {
+      const int32_t old_slot = slot_of(s.table[pg]);
+      const int32_t slot = p->alloc[0].refs[old_slot] > 1 ? p->alloc[0].take() : old_slot;
+      cuts.push_back({i, old_slot, slot});
+      ops.page({old_slot, slot, seq_ids[i] * MP + pg, static_cast<uint8_t>(p->page_fmt),
+                static_cast<uint8_t>(n_tokens[i] % kPageTokens), 0, 0});
+    }
+  }
+  if (rc == MKV_OK) rc = ops.flush();
+  if (rc == MKV_OK) commit(done, n_seqs);
+  for (; next < cuts.size(); ++next)  // a failed launch: the slots it would have used
+    if (cuts[next].new_slot != cuts[next].old_slot) p->alloc[0].give(cuts[next].new_slot);
+  for (int32_t e : dropped) p->alloc[slab_of(fmt_of(e))].give(slot_of(e));
+  return rc == MKV_OK ? ok() : rc;
+}
+
+int mkv_seq_free(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, void* stream) {
+  if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
+  if (n_seqs < 0 || (n_seqs > 0 && !seq_ids)) return fail(MKV_ERR_INVALID_ARG, "bad sequence list");
+  if (int e = check_seq_list(p, seq_ids, n_seqs, nullptr)) return e;
+  PageOps ops(p, "free launch", stream);
+  auto commit = [&](int32_t a, int32_t b) {
+    for (int32_t i = a; i < b; ++i) {
+      Seq& s = p->seqs[seq_ids[i]];
+      for (int32_t e : s.table) p->alloc[slab_of(fmt_of(e))].give(slot_of(e));
+      s = Seq();
+    }
+  };
+  int rc = MKV_OK;
+  int32_t done = 0;
+  for (int32_t i = 0; i < n_seqs && rc == MKV_OK; ++i) {
+    if (!ops.fits(0, 1)) {
+      if ((rc = ops.flush()) != MKV_OK) break;
+      commit(done, i);
+      done = i;
+    }
+    const int32_t pages = static_cast<int32_t>(p->seqs[seq_ids[i]].table.size());
+    if (pages > 0) ops.row({-1, seq_ids[i] * p->cfg.max_pages_per_seq, pages});
+  }
+  if (rc == MKV_OK) rc = ops.flush();
+  if (rc != MKV_OK) return rc;
+  commit(done, n_seqs);
+  return ok();
+}
+
+int mkv_pool_compact(mkv_pool_t p, int32_t* n_moved, void* stream) {
+  if (n_moved) *n_moved = 0;
+  if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
+  int rc = MKV_OK;
+  for (int f = 0; f < 2 && rc == MKV_OK; ++f) {
+    Allocator& a = p->alloc[f];
+    const int32_t held = a.n - a.n_free;
+    // ---- stage: held slots past the first `held` of the order move to the free slots among them
+    std::vector<uint64_t> from, to;  // (rank << 32) | slot, in the end both by rank
+    for (int32_t s = 0; s < a.n; ++s)
+      if ((a.rank[s] >= held) != (a.is_free[s] != 0))
+        (a.is_free[s] ? to : from).push_back((static_cast<uint64_t>(a.rank[s]) << 32) | static_cast<uint32_t>(s));
+    if (from.empty()) continue;
+    std::sort(from.begin(), from.end());
+    std::sort(to.begin(), to.end());
+    std::vector<int32_t> index(a.n, -1);  // a moving slot's place in the list
+    for (size_t k = 0; k < from.size(); ++k) index[static_cast<uint32_t>(from[k])] = static_cast<int32_t>(k);
+    struct Owner { int32_t seq, page; };
+    std::vector<Owner> owner(from.size());  // a sequence that holds it (the only one, or one of several)
+    for (int32_t q = 0; q < p->cfg.max_seqs; ++q) {
+      const std::vector<int32_t>& t = p->seqs[q].table;
+      for (size_t pg = 0; pg < t.size(); ++pg)
+        if (slab_of(fmt_of(t[pg])) == f && index[slot_of(t[pg])] >= 0)
+          owner[index[slot_of(t[pg])]] = {q, static_cast<int32_t>(pg)};
+    }
+    // ---- launch: each launch copies pages and publishes their entries, and counts as done when
+    // it was issued, so a later launch's failure leaves a pool that is compacted in part
+    const int fmt = f == 1 ? MKV_FMT_TQ3 : p->page_fmt;
+    PageOps ops(p, "compact launch", stream);
+    size_t done = 0;
+    for (size_t k = 0; k < from.size() && rc == MKV_OK; ++k) {
+      if (!ops.fits(1, 0)) {
+        if ((rc = ops.flush()) != MKV_OK) break;
+        done = k;
+      }
+      const int32_t src = static_cast<int32_t>(from[k] & 0xffffffffu), dst = static_cast<int32_t>(to[k] & 0xffffffffu);
+      const uint8_t shared = a.refs[src] > 1 ? 1 : 0;
+      ops.page({src, dst, shared ? owner[k].page : owner[k].seq * p->cfg.max_pages_per_seq + owner[k].page,
+                static_cast<uint8_t>(fmt), kPageTokens, shared, 0});
+    }
+    if (rc == MKV_OK && (rc = ops.flush()) == MKV_OK) done = from.size();
+    // ---- commit
+    for (Seq& s : p->seqs)
+      for (int32_t& e : s.table) {
+        if (slab_of(fmt_of(e)) != f) continue;
+        const int32_t k = index[slot_of(e)];
+        if (k >= 0 && static_cast<size_t>(k) < done)
+          e = entry_of(fmt, static_cast<int32_t>(to[k] & 0xffffffffu));
+      }
+    for (size_t k = 0; k < done; ++k) {
+      const int32_t src = static_cast<int32_t>(from[k] & 0xffffffffu), dst = static_cast<int32_t>(to[k] & 0xffffffffu);
+      a.refs[dst] = a.refs[src];
+      a.refs[src] = 0;
+      a.is_free[dst] = 0;
+      a.is_free[src] = 1;
+    }
+    a.rebuild();
+    if (n_moved) *n_moved += static_cast<int32_t>(done);
+  }
+  return rc == MKV_OK ? ok() : rc;
 }
 
 int mkv_get_block_table(mkv_pool_t p, int32_t seq, int32_t* host_out, int32_t cap,
@@ -1537,12 +1826,9 @@ int mkv_read_slot(mkv_pool_t p, int32_t entry, void* host_out, size_t cap, void*
 
 int mkv_pool_stats(mkv_pool_t p, int64_t* live, int32_t* n8, int32_t* n3, double* bpt) {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
-  int64_t tokens = 0, c8 = 0, c3 = 0;
-  for (const Seq& s : p->seqs) {
-    tokens += s.ctx;
-    c8 += static_cast<int64_t>(s.fp8_pages.size());
-    c3 += s.n3;
-  }
+  int64_t tokens = 0;  // (a page that sequences share counts once, a token in each of them)
+  for (const Seq& s : p->seqs) tokens += s.ctx;
+  const int64_t c8 = p->alloc[0].n - p->alloc[0].n_free, c3 = p->alloc[1].n - p->alloc[1].n_free;
   if (live) *live = tokens;
   if (n8) *n8 = static_cast<int32_t>(c8);
   if (n3) *n3 = static_cast<int32_t>(c3);

@@ -96,6 +96,7 @@ class RefPool:
         self.bf16_control = bf16_control
         self.bf16 = {}  # slot -> [kbits [Hkv,16,D] uint16, vbits]  (control pools)
         self.page_fmt = BF16 if bf16_control else FP8   # format of written (unconverted) pages
+        self.shared = {}  # (slab, slot) -> sequences that hold the slot, where more than one does
 
     # ------------------------------------------------------------------ helpers
     def _check_seq(self, s):
@@ -107,6 +108,20 @@ class RefPool:
 
     def _store(self, fmt):
         return {FP8: self.fp8, TQ3: self.tq3, BF16: self.bf16}[fmt]
+
+    def _release(self, fmt, slot):
+        """A sequence gives up a page: free when no other sequence holds it."""
+        key = (_slab(fmt), slot)
+        if key in self.shared:
+            self.shared[key] -= 1
+            if self.shared[key] == 1:
+                del self.shared[key]
+        else:
+            self._store(fmt).pop(slot)
+            self.alloc[_slab(fmt)].give(slot)
+
+    def _share(self, fmt, slot):
+        self.shared[_slab(fmt), slot] = self.shared.get((_slab(fmt), slot), 1) + 1
 
     def _new_page(self, seq):
         """Take a slot for a fresh written page (FP8, or BF16 in a control pool)."""
@@ -264,19 +279,22 @@ class RefPool:
             raise PoolError("INVALID_ARG", "repeated sequence or negative window")
         work = [] if self.bf16_control else [
             (s, p) for s in seq_ids for p in self.demote_candidates(s, window_tokens)]
-        if len(work) > len(self.alloc[TQ3].free):
+        if len({self.table[s][p] for s, p in work}) > len(self.alloc[TQ3].free):
             raise PoolError("OUT_OF_PAGES", "TQ3 pool exhausted")
-        done, freed = [], []
-        for s, p in work:
+        done, freed, converted = [], [], {}
+        for s, p in work:  # (a page that listed sequences share is converted once)
             _, src = self.table[s][p]
-            dst = self.alloc[TQ3].take()
-            self.tq3[dst] = self.convert(src)
+            if src in converted:
+                dst = converted[src]
+                self._share(TQ3, dst)
+            else:
+                dst = converted[src] = self.alloc[TQ3].take()
+                self.tq3[dst] = self.convert(src)
             self.table[s][p] = (TQ3, dst)
             done.append((s, p, src, dst))
             freed.append(src)
         for src in freed:
-            del self.fp8[src]
-            self.alloc[FP8].give(src)
+            self._release(FP8, src)
         return done
 
     def convert(self, fp8_slot):
@@ -294,8 +312,7 @@ class RefPool:
     def seq_reset(self, seq):
         self._check_seq(seq)
         for fmt, slot in self.table[seq]:
-            self._store(fmt).pop(slot)
-            self.alloc[_slab(fmt)].give(slot)
+            self._release(fmt, slot)
         self.table[seq] = []
         self.ctx[seq] = 0
         self.protected[seq] = set()
@@ -319,6 +336,118 @@ class RefPool:
             self.table[dst].append((fmt, new))
         self.ctx[dst] = self.ctx[src]
         self.protected[dst] = set(self.protected[src])
+
+    # ------------------------------------------------------------------ branches
+    def _cut(self, slot, kept):
+        """Zero the rows of a written page from ``kept`` on (its scales stay)."""
+        st = (self.bf16 if self.bf16_control else self.fp8)[slot]
+        for which in (0, 1):
+            st[which][:, kept:, :] = 0
+
+    def _private_copy(self, slot):
+        store = self._store(self.page_fmt)
+        new = self.alloc[0].take()
+        store[new] = [np.array(a, copy=True) for a in store[slot]]
+        return new
+
+    def fork(self, src_ids, dst_ids, n_tokens=None):
+        """Each empty ``dst`` holds the first tokens of its ``src``: full pages are the same
+        pages, a partial last page is a copy of its own, cut to the length."""
+        src_ids, dst_ids = [int(s) for s in src_ids], [int(d) for d in dst_ids]
+        for s in src_ids + dst_ids:
+            self._check_seq(s)
+        if len(set(dst_ids)) != len(dst_ids):
+            raise PoolError("INVALID_ARG", "repeated destination")
+        at = [self.ctx[s] for s in src_ids] if n_tokens is None else [int(n) for n in n_tokens]
+        need = 0
+        for s, d, n in zip(src_ids, dst_ids, at):
+            if d in src_ids or self.table[d] or self.ctx[d]:
+                raise PoolError("INVALID_ARG", "destination is not empty or a source")
+            if not 0 <= n <= self.ctx[s]:
+                raise PoolError("INVALID_ARG", "length")
+            if n % PAGE and self.table[s][n // PAGE][0] == TQ3:
+                raise PoolError("UNSUPPORTED", "cut inside a TQ3 page")
+            need += n % PAGE > 0
+        if need > len(self.alloc[0].free):
+            raise PoolError("OUT_OF_PAGES", "pool exhausted")
+        for s, d, n in zip(src_ids, dst_ids, at):
+            self.table[d] = list(self.table[s][:n // PAGE])
+            for fmt, slot in self.table[d]:
+                self._share(fmt, slot)
+            if n % PAGE:
+                new = self._private_copy(self.table[s][n // PAGE][1])
+                self._cut(new, n % PAGE)
+                self.table[d].append((self.page_fmt, new))
+            self.ctx[d] = n
+            self.protected[d] = {p for p in self.protected[s] if p < len(self.table[d])}
+
+    def truncate(self, seq_ids, n_tokens):
+        seq_ids, n_tokens = [int(s) for s in seq_ids], [int(n) for n in n_tokens]
+        for s in seq_ids:
+            self._check_seq(s)
+        if len(set(seq_ids)) != len(seq_ids) or any(n < 0 for n in n_tokens):
+            raise PoolError("INVALID_ARG", "repeated sequence or negative length")
+        copied = []
+        for s, n in zip(seq_ids, n_tokens):
+            if n > self.ctx[s]:
+                raise PoolError("INVALID_ARG", "longer than the sequence")
+            if n < self.ctx[s] and n % PAGE:
+                fmt, slot = self.table[s][n // PAGE]
+                if fmt == TQ3:
+                    raise PoolError("UNSUPPORTED", "cut inside a TQ3 page")
+                if (0, slot) in self.shared:
+                    copied.append(s)
+        if len(copied) > len(self.alloc[0].free):
+            raise PoolError("OUT_OF_PAGES", "pool exhausted")
+        given = []
+        for s, n in zip(seq_ids, n_tokens):
+            if n == self.ctx[s]:
+                continue
+            if n % PAGE:
+                fmt, slot = self.table[s][n // PAGE]
+                if s in copied:
+                    given.append((fmt, slot))
+                    slot = self._private_copy(slot)
+                    self.table[s][n // PAGE] = (fmt, slot)
+                self._cut(slot, n % PAGE)
+            keep = -(-n // PAGE)
+            given += self.table[s][keep:]
+            del self.table[s][keep:]
+            self.ctx[s] = n
+            self.protected[s] = {p for p in self.protected[s] if p < keep}
+        for fmt, slot in given:
+            self._release(fmt, slot)
+
+    def free(self, seq_ids):
+        seq_ids = [int(s) for s in seq_ids]
+        for s in seq_ids:
+            self._check_seq(s)
+        if len(set(seq_ids)) != len(seq_ids):
+            raise PoolError("INVALID_ARG", "repeated sequence")
+        for s in seq_ids:
+            self.seq_reset(s)
+
+    def compact(self):
+        """Held slots outside the first ones of the order move to the free slots among them."""
+        moved = 0
+        for slab, fmt in ((0, self.page_fmt), (1, TQ3)):
+            a, store = self.alloc[slab], self._store(fmt)
+            order = np.argsort(a.rank).tolist()
+            held = a.n - len(a.free)
+            src = [s for s in order[held:] if s not in a.free]
+            dst = [s for s in order[:held] if s in a.free]
+            to = dict(zip(src, dst))
+            moved += len(to)
+            for t in self.table:
+                t[:] = [(f, to.get(s, s)) if _slab(f) == slab else (f, s) for f, s in t]
+            for s, d in to.items():
+                store[d] = store.pop(s)
+                if (slab, s) in self.shared:
+                    self.shared[slab, d] = self.shared.pop((slab, s))
+            a.free = (a.free - set(dst)) | set(src)
+            a.heap = [(int(a.rank[s]), s) for s in a.free]
+            heapq.heapify(a.heap)
+        return moved
 
     # ------------------------------------------------------------------ views
     def slot_bytes(self, entry: int):
@@ -360,8 +489,8 @@ class RefPool:
 
     def stats(self):
         live = sum(self.ctx)
-        n8 = sum(1 for t in self.table for f, _ in t if f == self.page_fmt)
-        n3 = sum(1 for t in self.table for f, _ in t if f == TQ3)
+        n8 = len({e for t in self.table for e in t if e[0] == self.page_fmt})  # (a shared page once)
+        n3 = len({e for t in self.table for e in t if e[0] == TQ3})
         head = F.bf16_head_bytes(self.D) if self.bf16_control else F.fp8_head_bytes(self.D)
         kv_bytes = n8 * self.Hkv * head + n3 * self.Hkv * F.tq3_head_bytes(self.D)
         return live, n8, n3, (kv_bytes / live if live else 0.0)
