@@ -345,6 +345,26 @@ MKV_API int mkv_prefill_kv(mkv_pool_t pool, const int32_t* seq_ids, const int32_
                            int32_t n_seqs, const void* k_bf16, const void* v_bf16,
                            int32_t anchor_window_tokens, void* stream);
 
+/* Rotary positions with several axes (text; time, height and width of images and video), applied
+ * to q and k before mkv_prompt_attention, mkv_append_kv or mkv_prefill_kv.  For row r, every head
+ * and frequency i < n_freq, with angle = positions[axis_of[i]][r] * inv_freq[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ * where (a, b) are the channels (i, i + n_freq), or (2i, 2i + 1) when interleaved != 0.  Channels
+ * from 2 * n_freq on are copied.  The pool gives Hkv and D.
+ *   positions  device int32 [n_axes][rows]      inv_freq  device fp32 [n_freq], n_freq <= D / 2
+ *   axis_of    host [n_freq], each in [0, n_axes); NULL: axis 0 (n_axes <= 128)
+ *   q_in/q_out device bf16, rows of [num_q_heads][D], strides in elements; q_out may be q_in
+ *   k_in/k_out the same with Hkv heads
+ * An output overlaps no other array, but parts of one fused array may be rotated in place.  Any
+ * stride of at least a row and 2-byte alignment work; 16-byte aligned rows with n_freq a multiple
+ * of 8 are faster.  The angle is formed in 64 bits, so positions up to 2^31 keep their phase.
+ * Errors: INVALID_ARG, CUDA. */
+MKV_API int mkv_rope(mkv_pool_t pool, int64_t rows, const int32_t* positions, int32_t n_axes,
+                     const float* inv_freq, int32_t n_freq, const int32_t* axis_of, int32_t interleaved,
+                     const void* q_in, int64_t q_in_stride, void* q_out, int64_t q_out_stride,
+                     int32_t num_q_heads, const void* k_in, int64_t k_in_stride, void* k_out,
+                     int64_t k_out_stride, void* stream);
+
 /* Causal attention over whole prompts, for the prompt phase that precedes mkv_prefill_kv (decode
  * attends at most 32 query columns per KV head).  n_tokens (host, n_prompts entries, each >= 0)
  * are the lengths of prompts packed one after another without padding: prompt i takes the next

@@ -60,6 +60,8 @@ SIGNATURES = {
     "mkv_pool_compact": (ctypes.c_int, [_P, _I32P, _P]),
     "mkv_materialise_kv": (ctypes.c_int, [_P, _I32, _P, _P, ctypes.c_int64, _P]),
     "mkv_prefill_kv": (ctypes.c_int, [_P, _I32P, _I32P, _I32, _P, _P, _I32, _P]),
+    "mkv_rope": (ctypes.c_int, [_P, _I64, _P, _I32, _P, _I32, _I32P, _I32, _P, _I64, _P, _I64, _I32,
+                                _P, _I64, _P, _I64, _P]),
     "mkv_prompt_attention": (ctypes.c_int, [_P, _I32P, _I32, _P, _I64, _P, _I64, _P, _I64, _I32,
                                             ctypes.c_float, _P, _P]),
     "mkv_selftest_wait": (ctypes.c_int, [_P, ctypes.c_int64, _P]),
@@ -310,6 +312,41 @@ class Pool:
         import torch
         s = stream if stream is not None else torch.cuda.current_stream(self.buffers[0].device)
         return ctypes.c_void_p(s.cuda_stream)
+
+    def rope(self, q, k, positions, inv_freq, axes=None, interleaved=False, q_out=None, k_out=None,
+             stream=None):
+        """Rotate q bf16 [rows, Hq, D] and k bf16 [rows, Hkv, D] (rows may be strided) by
+        ``positions`` (int32 [rows] or [n_axes, rows]) times ``inv_freq`` (fp32 [n_freq]); ``axes``
+        lists the axis of each frequency (default: axis 0).  Pairs are channels n_freq apart, or
+        neighbours when ``interleaved``.  Returns (q_out, k_out): new tensors unless given; the
+        inputs themselves for a rotation in place (mkv_rope)."""
+        import torch
+        if self.host_only:
+            raise ValueError("host-only pools have no device")
+        dev = self.buffers[0].device
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [rows, Hq, head_dim]")
+        rows, Hq = q.shape[0], q.shape[1]
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format) if k_out is None else k_out
+        (qp, qs), (kp, ks), (qo, qos), (ko, kos) = (
+            _rows_ptr(t, h, self.D, name, dev) for t, h, name in
+            ((q, Hq, "q"), (k, self.Hkv, "k"), (q_out, Hq, "q_out"), (k_out, self.Hkv, "k_out")))
+        pp, fp = _dev_ptr(positions, torch.int32, "positions"), _dev_ptr(inv_freq, torch.float32, "inv_freq")
+        pos_shape = tuple(positions.shape) if positions.dim() == 2 else (1,) + tuple(positions.shape)
+        if len(pos_shape) != 2 or pos_shape[1] != rows or inv_freq.dim() != 1:
+            raise ValueError(f"positions must be [{rows}] or [n_axes, {rows}], inv_freq [n_freq]")
+        if any(t.shape[0] != rows for t in (k, q_out, k_out)):
+            raise ValueError(f"q, k and the outputs must all have {rows} rows")
+        if positions.device != dev or inv_freq.device != dev:
+            raise ValueError(f"positions and inv_freq must be on {dev}")
+        a, ap = (None, None) if axes is None else _i32_array(axes)
+        if a is not None and a.size != inv_freq.numel():
+            raise ValueError("axes must list an axis per frequency")
+        _check(lib().mkv_rope(self.handle, rows, pp, pos_shape[0], fp, inv_freq.numel(), ap,
+                              1 if interleaved else 0, qp, qs, qo, qos, Hq, kp, ks, ko, kos,
+                              self._stream(stream)), "mkv_rope")
+        return q_out, k_out
 
     def prompt_attention(self, q, k, v, n_tokens, sm_scale=None, out=None, stream=None):
         """Causal attention over packed prompts of ``n_tokens`` tokens each: q bf16 [rows, Hq, D],

@@ -210,6 +210,22 @@ struct PromptInputs {
   int64_t rows;                         // packed rows of all prompts
 };
 
+// ------------------------------------------------------------------ rotary positions
+struct RopeParams {
+  const uint16_t *q_in, *k_in;  // bf16 bits, rows of H heads of D
+  uint16_t *q_out, *k_out;
+  int64_t q_in_stride, k_in_stride, q_out_stride, k_out_stride;  // elements between rows
+  const int32_t* positions;     // [axes][rows]
+  const float* inv_freq;        // [half]
+  int64_t rows;
+  int32_t Hq, Hkv, D;
+  int32_t half;      // frequencies: the first 2 * half channels of a head are rotated
+  int32_t next;      // 1: pairs of neighbouring channels, 0: of channels `half` apart
+  int32_t vec;       // 1: 16-byte vectors (alignment and sizes checked on the host)
+  int32_t cta_rows;  // rows of a CTA (set by the launcher)
+  uint8_t axis[128]; // axis of each frequency
+};
+
 // Every parameter block fits the 32,764-byte kernel-parameter limit.
 static_assert(sizeof(AppendParams) <= 32764 && sizeof(DemoteParams) <= 32764 &&
                   sizeof(RetagParams) <= 32764 && sizeof(PackParams) <= 32764 &&
@@ -223,6 +239,7 @@ cudaError_t launch_page_ops(PageOpParams& p, cudaStream_t s);
 cudaError_t launch_materialise(const MaterialiseParams& p, cudaStream_t s);
 cudaError_t launch_pack(const PackParams& p, cudaStream_t s);
 cudaError_t launch_prompt(const PromptParams& p, const PromptInputs& in, cudaStream_t s);
+cudaError_t launch_rope(RopeParams& p, cudaStream_t s);
 int prompt_tiles_per_unit(int D);  // 128-row query tiles of a unit
 cudaError_t launch_partial(const DecodeParams& p, cudaStream_t s);
 cudaError_t launch_merge(const DecodeParams& p, cudaStream_t s);

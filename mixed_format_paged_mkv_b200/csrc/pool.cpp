@@ -226,6 +226,28 @@ int validate_config(const mkv_pool_config* c) {
   return MKV_OK;
 }
 
+// Rows of a strided 2-byte array: `width` elements every `stride`.
+struct RowSpan {
+  const char* name;
+  const void* ptr;
+  int64_t stride, width;
+};
+// The address ranges from first to last element touch.
+bool ranges_overlap(const RowSpan& a, int64_t a_rows, const RowSpan& b, int64_t b_rows) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.ptr), b0 = reinterpret_cast<uintptr_t>(b.ptr);
+  return a0 < b0 + ((b_rows - 1) * b.stride + b.width) * 2 && b0 < a0 + ((a_rows - 1) * a.stride + a.width) * 2;
+}
+// Some element lies in both.  Parts of one array (equal strides) may alternate: they are apart when
+// their columns are.
+bool rows_overlap(const RowSpan& a, const RowSpan& b, int64_t rows) {
+  if (!ranges_overlap(a, rows, b, rows)) return false;
+  if (a.stride != b.stride) return true;
+  const int64_t step = a.stride * 2;
+  int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.ptr) - reinterpret_cast<uintptr_t>(a.ptr)) % step;
+  if (d < 0) d += step;
+  return d < a.width * 2 || step - d < b.width * 2;
+}
+
 // Makes the pool's device current for the calls that take tensors of their own.
 struct DeviceGuard {
   int before = 0;
@@ -1247,6 +1269,76 @@ int mkv_seq_reset(mkv_pool_t p, int32_t seq, void* stream) {
   return ok();
 }
 
+int mkv_rope(mkv_pool_t p, int64_t rows, const int32_t* positions, int32_t n_axes, const float* inv_freq,
+             int32_t n_freq, const int32_t* axis_of, int32_t interleaved, const void* q_in, int64_t q_in_stride,
+             void* q_out, int64_t q_out_stride, int32_t Hq, const void* k_in, int64_t k_in_stride, void* k_out,
+             int64_t k_out_stride, void* stream) {
+  if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
+  const int Hkv = p->cfg.num_kv_heads, D = p->cfg.head_dim;
+  if (rows < 0 || rows > INT32_MAX) return fail(MKV_ERR_INVALID_ARG, "rows out of range");
+  if (Hq < Hkv || Hq % Hkv) return fail(MKV_ERR_INVALID_ARG, "num_q_heads %d not a multiple of Hkv %d", Hq, Hkv);
+  if (n_axes < 1 || n_axes > 128) return fail(MKV_ERR_INVALID_ARG, "n_axes must be in [1, 128]");
+  if (n_freq < 1 || 2 * static_cast<int64_t>(n_freq) > D)
+    return fail(MKV_ERR_INVALID_ARG, "n_freq %d outside [1, head_dim / 2]", n_freq);
+  for (int32_t i = 0; axis_of && i < n_freq; ++i)
+    if (axis_of[i] < 0 || axis_of[i] >= n_axes)
+      return fail(MKV_ERR_INVALID_ARG, "axis %d of frequency %d outside [0, %d)", axis_of[i], i, n_axes);
+  if (rows == 0) return ok();
+  if (!positions || !inv_freq || !q_in || !q_out || !k_in || !k_out)
+    return fail(MKV_ERR_INVALID_ARG, "positions, inv_freq, q or k is NULL");
+  if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(inv_freq)) & 3)
+    return fail(MKV_ERR_INVALID_ARG, "positions and inv_freq must be 4-byte aligned");
+  const RowSpan span[4] = {{"q_in", q_in, q_in_stride, static_cast<int64_t>(Hq) * D},
+                           {"k_in", k_in, k_in_stride, static_cast<int64_t>(Hkv) * D},
+                           {"q_out", q_out, q_out_stride, static_cast<int64_t>(Hq) * D},
+                           {"k_out", k_out, k_out_stride, static_cast<int64_t>(Hkv) * D}};
+  int64_t bits = 0;
+  for (const RowSpan& x : span) {
+    if (x.stride < x.width || x.stride >= (1LL << 38))
+      return fail(MKV_ERR_INVALID_ARG, "%s: row stride %lld below a row's %lld elements", x.name,
+                  static_cast<long long>(x.stride), static_cast<long long>(x.width));
+    if (reinterpret_cast<uintptr_t>(x.ptr) & 1) return fail(MKV_ERR_INVALID_ARG, "%s must be 2-byte aligned", x.name);
+    bits |= reinterpret_cast<uintptr_t>(x.ptr) | (x.stride * 2);
+  }
+  for (int o = 2; o < 4; ++o)
+    for (int i = 0; i < 4; ++i) {
+      if (i >= o) continue;
+      const bool in_place = i == o - 2 && span[i].ptr == span[o].ptr && span[i].stride == span[o].stride;
+      if (!in_place && rows_overlap(span[i], span[o], rows))
+        return fail(MKV_ERR_INVALID_ARG, "%s overlaps %s", span[o].name, span[i].name);
+    }
+  const RowSpan tables[2] = {{"positions", positions, 2 * rows * n_axes, 2 * rows * n_axes},
+                             {"inv_freq", inv_freq, 2 * n_freq, 2 * n_freq}};
+  for (const RowSpan& t : tables)
+    for (int o = 2; o < 4; ++o)
+      if (ranges_overlap(t, 1, span[o], rows)) return fail(MKV_ERR_INVALID_ARG, "%s overlaps %s", span[o].name, t.name);
+  if (p->host_only) return fail(MKV_ERR_INVALID_ARG, "host-only pool has no device");
+  RopeParams prm{};
+  prm.q_in = static_cast<const uint16_t*>(q_in);
+  prm.k_in = static_cast<const uint16_t*>(k_in);
+  prm.q_out = static_cast<uint16_t*>(q_out);
+  prm.k_out = static_cast<uint16_t*>(k_out);
+  prm.q_in_stride = q_in_stride;
+  prm.k_in_stride = k_in_stride;
+  prm.q_out_stride = q_out_stride;
+  prm.k_out_stride = k_out_stride;
+  prm.positions = positions;
+  prm.inv_freq = inv_freq;
+  prm.rows = rows;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.D = D;
+  prm.half = n_freq;
+  prm.next = interleaved ? 1 : 0;
+  prm.vec = (bits & 15) == 0 && n_freq % 8 == 0 ? 1 : 0;
+  for (int32_t i = 0; axis_of && i < n_freq; ++i) prm.axis[i] = static_cast<uint8_t>(axis_of[i]);
+  const DeviceGuard guard(p->device);
+  const cudaError_t e = launch_rope(prm, as_stream(stream));
+  ++p->launches;
+  if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+  return ok();
+}
+
 int mkv_prompt_attention(mkv_pool_t p, const int32_t* n_tokens, int32_t n_prompts, const void* q_bf16,
                          int64_t q_stride, const void* k_bf16, int64_t k_stride, const void* v_bf16,
                          int64_t v_stride, int32_t Hq, float sm_scale, void* out_bf16, void* stream) try {
@@ -1267,21 +1359,19 @@ int mkv_prompt_attention(mkv_pool_t p, const int32_t* n_tokens, int32_t n_prompt
   if (rows > INT32_MAX) return fail(MKV_ERR_INVALID_ARG, "too many tokens");
   if (rows == 0) return ok();
   if (!q_bf16 || !k_bf16 || !v_bf16 || !out_bf16) return fail(MKV_ERR_INVALID_ARG, "q/k/v/out is NULL");
-  struct Input { const char* name; const void* ptr; int64_t stride, width; };
-  const Input in[3] = {{"q", q_bf16, q_stride, static_cast<int64_t>(Hq) * D},
-                       {"k", k_bf16, k_stride, static_cast<int64_t>(Hkv) * D},
-                       {"v", v_bf16, v_stride, static_cast<int64_t>(Hkv) * D}};
-  const uintptr_t o0 = reinterpret_cast<uintptr_t>(out_bf16), o1 = o0 + rows * in[0].width * 2;
-  for (const Input& x : in) {
+  const RowSpan in[3] = {{"q", q_bf16, q_stride, static_cast<int64_t>(Hq) * D},
+                         {"k", k_bf16, k_stride, static_cast<int64_t>(Hkv) * D},
+                         {"v", v_bf16, v_stride, static_cast<int64_t>(Hkv) * D}};
+  const RowSpan out{"out", out_bf16, in[0].width, in[0].width};
+  for (const RowSpan& x : in) {
     if (x.stride < x.width || x.stride % 8 || x.stride >= (1LL << 38))
       return fail(MKV_ERR_INVALID_ARG, "%s: row stride %lld must be a multiple of 8 elements, at least %lld", x.name,
                   static_cast<long long>(x.stride), static_cast<long long>(x.width));
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(x.ptr);
-    if (a0 & 15) return fail(MKV_ERR_INVALID_ARG, "%s must be 16-byte aligned", x.name);
-    if (a0 < o1 && o0 < a0 + ((rows - 1) * x.stride + x.width) * 2)
-      return fail(MKV_ERR_INVALID_ARG, "out overlaps %s", x.name);
+    if (reinterpret_cast<uintptr_t>(x.ptr) & 15)
+      return fail(MKV_ERR_INVALID_ARG, "%s must be 16-byte aligned", x.name);
+    if (ranges_overlap(x, rows, out, rows)) return fail(MKV_ERR_INVALID_ARG, "out overlaps %s", x.name);
   }
-  if (o0 & 15) return fail(MKV_ERR_INVALID_ARG, "out must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(out_bf16) & 15) return fail(MKV_ERR_INVALID_ARG, "out must be 16-byte aligned");
   if (p->host_only) return fail(MKV_ERR_INVALID_ARG, "host-only pool cannot attend");
 
   // ---- the prompts, longest first (the CTAs start in this order), in launches of whole prompts

@@ -1,0 +1,164 @@
+// Rotary positions with several axes (mkv_rope).
+//
+// Frequency i < R/2 of a head rotates the channel pair (a, b) = (x[i], x[i + R/2]) or, with
+// neighbouring pairs, (x[2i], x[2i + 1]) by the angle pos[axis(i)][row] * inv_freq[i]:
+//   a' = a cos - b sin,  b' = b cos + a sin;  channels from R on are passed through.
+//
+// The angle is formed in fp64 (a position up to 2^31 times an fp32 frequency is exact to 2^-53, so
+// it is known to about 1e-7 rad at any position), reduced to a fraction of a turn and only then
+// rounded to fp32 for the sine and cosine.  The rotation itself is fp32, rounded once to bf16.
+//
+// Bound by memory: q and k are read and written once.  A CTA takes a few rows: its threads first
+// load their vectors, then compute the rows' sines and cosines into shared memory (each angle once
+// for all heads) while the loads are in flight, then rotate and store.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "device_util.cuh"
+#include "mkv_internal.h"
+
+namespace mkv {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void sincos_turns(int32_t pos, float inv_freq, float* s, float* c) {
+  constexpr double kInvTwoPi = 0.15915494309189533577;
+  const double turns = static_cast<double>(pos) * static_cast<double>(inv_freq) * kInvTwoPi;
+  sincospif(2.0f * static_cast<float>(turns - rint(turns)), s, c);
+}
+
+// The sines and cosines of `rows` rows from row0 on, [row][frequency].
+__device__ __forceinline__ void fill_table(const RopeParams& p, int64_t row0, int rows, float* sn, float* cs) {
+  for (int i = threadIdx.x; i < rows * p.half; i += kThreads) {
+    const int f = i % p.half;
+    const int32_t pos = p.positions[p.axis[f] * p.rows + row0 + i / p.half];
+    sincos_turns(pos, p.inv_freq[f], &sn[i], &cs[i]);
+  }
+}
+
+__device__ __forceinline__ void rotate(uint32_t& a, uint32_t& b, const float* s, const float* c) {
+  const float a0 = bf16_lo(a), a1 = bf16_hi(a), b0 = bf16_lo(b), b1 = bf16_hi(b);
+  a = pack_bf16x2(fmaf(a0, c[0], -b0 * s[0]), fmaf(a1, c[1], -b1 * s[1]));
+  b = pack_bf16x2(fmaf(b0, c[0], a0 * s[0]), fmaf(b1, c[1], a1 * s[1]));
+}
+// A word that holds a whole pair.
+__device__ __forceinline__ void rotate_word(uint32_t& w, float s, float c) {
+  const float a = bf16_lo(w), b = bf16_hi(w);
+  w = pack_bf16x2(fmaf(a, c, -b * s), fmaf(b, c, a * s));
+}
+
+// 16-byte vectors.  A unit is 16 channels: the vectors of 8 pairs (x[8u..], x[R/2 + 8u..]), two
+// neighbouring vectors with neighbouring pairs, or two neighbouring vectors that pass through.
+template <bool NEXT>
+__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int U = 4;  // units a thread loads before the angles are needed
+  extern __shared__ __align__(16) float table[];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.cta_rows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.cta_rows), p.rows - row0));
+  float* sn = table;
+  float* cs = table + p.cta_rows * p.half;
+  const int heads = p.Hq + p.Hkv, per = p.D / 16, rot = p.half / 8;  // units a head, of which rotated
+  const int units = rows * heads * per;
+  bool have_table = false;
+  for (int u0 = threadIdx.x; u0 < units || !have_table; u0 += U * kThreads) {
+    uint4 a[U], b[U];
+    uint4* oa[U];
+    int step[U];  // vectors from a unit's first to its second; 0: no unit
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      const int u = u0 + e * kThreads;
+      step[e] = 0;
+      if (u >= units) continue;
+      const int c = u % per, h = u / per % heads;
+      const int64_t r = row0 + u / per / heads;
+      const bool is_q = h < p.Hq;
+      const int hh = is_q ? h : h - p.Hq;
+      const int first = NEXT || c >= rot ? 2 * c : c;
+      step[e] = NEXT || c >= rot ? 1 : p.half / 8;
+      const uint4* in = reinterpret_cast<const uint4*>(
+          (is_q ? p.q_in + r * p.q_in_stride : p.k_in + r * p.k_in_stride) + hh * p.D) + first;
+      oa[e] = reinterpret_cast<uint4*>(
+          (is_q ? p.q_out + r * p.q_out_stride : p.k_out + r * p.k_out_stride) + hh * p.D) + first;
+      a[e] = in[0];
+      b[e] = in[step[e]];
+    }
+    if (!have_table) {
+      fill_table(p, row0, rows, sn, cs);
+      __syncthreads();
+      have_table = true;
+    }
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      if (step[e] == 0) continue;
+      const int u = u0 + e * kThreads;
+      const int c = u % per, r = u / per / heads;
+      if (c < rot) {
+        float s[8], k[8];
+        const float4* s4 = reinterpret_cast<const float4*>(sn + r * p.half + 8 * c);
+        const float4* c4 = reinterpret_cast<const float4*>(cs + r * p.half + 8 * c);
+        *reinterpret_cast<float4*>(s) = s4[0];
+        *reinterpret_cast<float4*>(s + 4) = s4[1];
+        *reinterpret_cast<float4*>(k) = c4[0];
+        *reinterpret_cast<float4*>(k + 4) = c4[1];
+        if (NEXT) {
+          rotate_word(a[e].x, s[0], k[0]);
+          rotate_word(a[e].y, s[1], k[1]);
+          rotate_word(a[e].z, s[2], k[2]);
+          rotate_word(a[e].w, s[3], k[3]);
+          rotate_word(b[e].x, s[4], k[4]);
+          rotate_word(b[e].y, s[5], k[5]);
+          rotate_word(b[e].z, s[6], k[6]);
+          rotate_word(b[e].w, s[7], k[7]);
+        } else {
+          rotate(a[e].x, b[e].x, s, k);
+          rotate(a[e].y, b[e].y, s + 2, k + 2);
+          rotate(a[e].z, b[e].z, s + 4, k + 4);
+          rotate(a[e].w, b[e].w, s + 6, k + 6);
+        }
+      }
+      oa[e][0] = a[e];
+      oa[e][step[e]] = b[e];
+    }
+  }
+}
+
+// Any even R, alignment and stride: one pair (or two channels that pass through) at a time.
+__global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ __align__(16) float table[];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.cta_rows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.cta_rows), p.rows - row0));
+  float* sn = table;
+  float* cs = table + p.cta_rows * p.half;
+  fill_table(p, row0, rows, sn, cs);
+  __syncthreads();
+  const int heads = p.Hq + p.Hkv, per = p.D / 2;
+  for (int u = threadIdx.x; u < rows * heads * per; u += kThreads) {
+    const int c = u % per, h = u / per % heads, lr = u / per / heads;
+    const int64_t r = row0 + lr;
+    const bool is_q = h < p.Hq;
+    const int hh = is_q ? h : h - p.Hq;
+    const uint16_t* in = (is_q ? p.q_in + r * p.q_in_stride : p.k_in + r * p.k_in_stride) + hh * p.D;
+    uint16_t* out = (is_q ? p.q_out + r * p.q_out_stride : p.k_out + r * p.k_out_stride) + hh * p.D;
+    const int i0 = c >= p.half || p.next ? 2 * c : c, i1 = c >= p.half || p.next ? 2 * c + 1 : c + p.half;
+    uint32_t w = in[i0] | static_cast<uint32_t>(in[i1]) << 16;
+    if (c < p.half) rotate_word(w, sn[lr * p.half + c], cs[lr * p.half + c]);
+    out[i0] = static_cast<uint16_t>(w);
+    out[i1] = static_cast<uint16_t>(w >> 16);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(RopeParams& p, cudaStream_t s) {
+  if (p.rows <= 0) return cudaSuccess;
+  p.cta_rows = 1;
+  const unsigned grid = static_cast<unsigned>((p.rows + p.cta_rows - 1) / p.cta_rows);
+  const size_t smem = sizeof(float) * 2 * p.cta_rows * p.half;
+  if (!p.vec) rope_any_kernel<<<grid, kThreads, smem, s>>>(p);
+  else if (p.next) rope_vec_kernel<true><<<grid, kThreads, smem, s>>>(p);
+  else rope_vec_kernel<false><<<grid, kThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace mkv
