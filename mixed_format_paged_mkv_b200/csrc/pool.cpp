@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstring>
 #include <functional>
+#include <limits>
 #include <memory>
 #include <new>
 #include <string>
@@ -1386,7 +1387,9 @@ int mkv_prompt_attention(mkv_pool_t p, const int32_t* n_tokens, int32_t n_prompt
   prm->v = static_cast<const uint16_t*>(v_bf16);
   prm->v_stride = v_stride;
   prm->status = p->d_status;
-  prm->c = sm_scale * 1.4426950408889634f;
+  // (a scale of zero weighs all keys alike; the smallest normal value does too and keeps masked
+  // scores at -inf)
+  prm->c = std::max(sm_scale * 1.4426950408889634f, std::numeric_limits<float>::min());
   prm->Hkv = Hkv;
   prm->Hq = Hq;
   prm->g = g;

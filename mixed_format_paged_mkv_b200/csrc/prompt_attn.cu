@@ -13,9 +13,10 @@
 // Roles (one CTA per SM):
 //   softmax warps  4 per tile, one row per thread: scores from tensor memory, probabilities back
 //                  into it as bf16, running sum and reference in registers, output at the end
-//   producer       one thread: tensor-map loads of Q and of K/V chunks into a ring
-//   MMA            one thread: S = Q K^T and O += P V (P read from tensor memory)
-//   guard (2 warps) on chunks that the causal line or the prompt's end crosses: zeroes V rows past
+//   producer       tensor-map loads of Q and of K/V chunks into a ring
+//   MMA            a warp per tile, one lane of which issues S = Q K^T and O += P V (P is read from
+//                  tensor memory)
+//   guard          on V chunks that the causal line or the prompt's end crosses: zeroes V rows past
 //                  the end and replaces non-finite V elements by zero, because 0 x inf would reach
 //                  rows that do not see them; the rows that do see them get them back at the end
 //
@@ -39,34 +40,64 @@ template <int D_>
 struct Cfg {
   static constexpr int D = D_;
   static constexpr int NT = D == 256 ? 1 : 2;     // query tiles of an item
-  static constexpr int SB = D == 256 ? 2 : 1;     // score buffers per tile
-  static constexpr int CK = D == 256 ? 64 : 128;  // keys of a K or V chunk
-  static constexpr int HALVES = 128 / CK;         // chunks of a 128-key tile
+  static constexpr int SB = 2;                    // score buffers per tile
+  static constexpr int KT = D == 256 ? 128 : 64;  // keys of a step (of a score buffer)
+  static constexpr int PH = KT / 64;              // the probabilities of a step are handed on by 64 keys
   static constexpr int BLK = D / 64;              // 64-channel blocks (128 bytes: the swizzle span)
-  static constexpr int STAGES = D == 64 ? 8 : 5;
+  // ring chunks: K of a step in KC chunks of all its keys and KB blocks each, V in VC chunks of VK
+  // keys and all channels
+  static constexpr int KC = D == 256 ? 2 : 1, KB = BLK / KC;
+  static constexpr int VC = D == 256 ? 2 : 1, VK = KT / VC;
+  static constexpr int K_BLOCK = KT * 128, V_BLOCK = VK * 128;
+  static constexpr int CHUNK = KB * K_BLOCK;
+  static_assert(CHUNK == BLK * V_BLOCK, "K and V chunks share the ring");
+  static constexpr int STAGES = D == 64 ? 16 : D == 128 ? 10 : 5;
   static constexpr int Q_BLOCK = 128 * 128;
   static constexpr int Q_TILE = BLK * Q_BLOCK;
-  static constexpr int KV_BLOCK = CK * 128;
-  static constexpr int CHUNK = BLK * KV_BLOCK;
   static constexpr int SMEM_Q = NT * Q_TILE;
-  static constexpr int SMEM = SMEM_Q + STAGES * CHUNK + 1024 /* alignment */ + 512 /* barriers */;
-  static constexpr int SOFT_WARPS = 4 * NT;
-  static constexpr int THREADS = 32 * (SOFT_WARPS + 4);
-  static constexpr uint32_t IDESC_S = tc_idesc_bf16(128, CK, false);
+  static constexpr int SMEM = SMEM_Q + STAGES * CHUNK + 1024 /* alignment */ + 1024 /* barriers */;
+  // warps: softmax (4 a tile), producer, guard, MMA (1 a tile)
+  static constexpr int PRODUCER = 4 * NT, GUARD = PRODUCER + 1, MMA = GUARD + 1;
+  static constexpr int WARPS = MMA + NT, THREADS = 32 * WARPS;
+  static constexpr uint32_t IDESC_S = tc_idesc_bf16(128, KT, false);
   static constexpr uint32_t IDESC_PV = tc_idesc_bf16(128, D, true);
+  static constexpr int POLY = D == 64 ? 4 : 0;  // of 16 pairs of scores, those that poly_exp2 takes
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
+// Descriptors without their start address: K-major rows, and V's rows that run along the channels.
+constexpr uint64_t kDescK = tc_smem_desc(0, 16, 1024);
+template <class C>
+constexpr uint64_t kDescV = tc_smem_desc(0, C::V_BLOCK, 1024);
 constexpr uint32_t kOutCol = 256;       // first output column in tensor memory
 constexpr float kRescaleAbove = 8.0f;   // log2 units a row's maximum may exceed its reference by
 constexpr int kFlagSlots = 8;           // items the guard may run ahead of the softmax warps
 
+// Position in the ring of chunks: the stage, and how often the ring went round.
+template <int STAGES>
+struct Ring {
+  uint32_t stage = 0, round = 0;
+  __device__ __forceinline__ void step() {
+    if (++stage == STAGES) {
+      stage = 0;
+      ++round;
+    }
+  }
+  __device__ __forceinline__ Ring plus(int n) const {
+    Ring r = *this;
+    for (int i = 0; i < n; ++i) r.step();
+    return r;
+  }
+};
+
 template <class C>
 struct Bars {
   uint64_t q_full, q_empty;
-  uint64_t kv_full[C::STAGES], kv_empty[C::STAGES], v_ready[C::STAGES];
-  uint64_t s_full[C::NT * C::SB], p_full[C::NT * C::SB];
-  uint64_t o_done[C::NT], o_free[C::NT];
+  uint64_t kv_full[C::STAGES], kv_empty[C::STAGES], v_guard[C::STAGES], v_ready[C::STAGES];
+  uint64_t s_full[C::NT * C::SB], p_full[C::NT * C::SB][C::PH], o_done[C::NT * C::SB];
+  uint64_t o_free[C::NT];
+  uint64_t next_full[2], next_empty[2];
+  uint4 next[2];            // answers that name the next items
   uint32_t tmem;
   int32_t abort;
   int32_t bad[kFlagSlots];  // item number whose V had a non-finite element on a guarded chunk
@@ -77,8 +108,8 @@ struct Item {
   int row0, len, t0, h;  // first packed row and length of the prompt, first token, KV head
 };
 
-__device__ __forceinline__ bool get_item(const PromptParams& p, int NT, int64_t index, Item& it) {
-  if (index >= static_cast<int64_t>(p.n_units) * p.Hkv) return false;
+__device__ __forceinline__ Item get_item(const PromptParams& p, int NT, int64_t index) {
+  Item it;
   const int u = static_cast<int>(index / p.Hkv);
   it.h = static_cast<int>(index % p.Hkv);
   int lo = 0, hi = p.n_seqs - 1;  // the prompt whose units include u
@@ -90,35 +121,75 @@ __device__ __forceinline__ bool get_item(const PromptParams& p, int NT, int64_t 
   it.row0 = p.seq[lo].row0;
   it.len = p.seq[lo].len;
   it.t0 = (p.seq[lo].unit_end - 1 - u) * NT * p.tile_tokens;  // last tokens (most keys) first
-  return true;
+  return it;
 }
 
-// 128-key tiles that query tile t of an item visits (0: the tile has no tokens).
-__device__ __forceinline__ int key_tiles(const Item& it, int t, int TT) {
+// Steps of KT keys that query tile t of an item visits (0: the tile has no tokens).
+template <class C>
+__device__ __forceinline__ int key_steps(const Item& it, int t, int TT) {
   const int t0 = it.t0 + t * TT;
-  return t0 < it.len ? (min(it.len, t0 + TT) + 127) >> 7 : 0;
+  return t0 < it.len ? (min(it.len, t0 + TT) + C::KT - 1) / C::KT : 0;
 }
 
-// A chunk that starts at key c0 needs the guard: some row of the item does not see all its keys.
+// A V chunk that starts at key c0 needs the guard: some row of the item does not see all its keys.
 template <class C>
 __device__ __forceinline__ bool guarded(const Item& it, int c0) {
-  return c0 + C::CK > it.t0 + 1;
+  return c0 + C::VK > it.t0 + 1;
 }
 
-// Bounded wait that also ends when another warp gave up; false: leave the role's loops.
-template <class B>
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, B* b, int32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+// Bounded wait of one thread that also ends when another warp gave up; false: leave the role's
+// loops.  An attempt suspends the thread for up to 50 us, so that waiting warps leave the issue slots
+// and the shared-memory pipe to the others.  Reading the timer takes longer than most waits, so the
+// first attempts do without.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status) {
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait_sleep(bar, parity, 50000u)) return true;
   const uint64_t start = global_timer_ns();
   for (;;) {
-    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-    if (*reinterpret_cast<volatile int32_t*>(&b->abort)) return false;
+    if (mbar_try_wait_sleep(bar, parity, 50000u)) return true;
+    if (*reinterpret_cast<volatile int32_t*>(abort)) return false;
     if (global_timer_ns() - start > 2000000000ull) {
-      *reinterpret_cast<volatile int32_t*>(&b->abort) = 1;
+      *reinterpret_cast<volatile int32_t*>(abort) = 1;
       flag_status(status, kStatusTimeout);
       return false;
     }
   }
+}
+template <class B>
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, B* b, int32_t* status) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, &b->abort, status);
+}
+// The same for a whole warp: where the first attempt fails, one lane waits and the others follow it.
+template <class B>
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, B* b, int32_t* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_slow(bar, parity, &b->abort, status);
+  return __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+}
+// For the warp that feeds the tensor core: it spins for a while, since waking up costs more.
+template <class B>
+__device__ __forceinline__ bool wait_spin(uint64_t* bar, uint32_t parity, B* b, int32_t* status) {
+#pragma unroll 1
+  for (int i = 0; i < 1000; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_bar_warp(bar, parity, b, status);
+}
+
+// Index of the CTA's n-th item, -1: none (or a wait gave up).  Called by a whole warp or by one
+// thread of it; either counts once on next_empty.
+template <bool ONE, class B>
+__device__ __forceinline__ int64_t next_item(int n, B* b, int32_t* status) {
+  if (n == 0) return blockIdx.x;
+  const int s = (n - 1) & 1;
+  uint64_t* bar = &b->next_full[s];
+  const uint32_t parity = ((n - 1) >> 1) & 1;
+  if (!(ONE ? wait_bar(bar, parity, b, status) : wait_bar_warp(bar, parity, b, status))) return -1;
+  const int64_t index = clc_answer(&b->next[s]);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // this read, then the next answer
+  if (!ONE) __syncwarp();
+  if (ONE || (threadIdx.x & 31) == 0) mbar_arrive(&b->next_empty[s]);
+  return index;
 }
 
 // 8 bf16 values: whether one is infinite or NaN.
@@ -134,41 +205,65 @@ __device__ __forceinline__ uint32_t zero_nonfinite(uint32_t w) {
   return w;
 }
 
+// 2^x of two values, x <= 8, with the FMA pipe: x = n + r with n the nearest integer (the sum with
+// 1.5 2^23 + 127 rounds to it and leaves n + 127 in the low mantissa bits, from where a shift makes it
+// the exponent of 2^n), 2^r by a polynomial of degree 4 on [-1/2, 1/2] (minimax for the relative error
+// by the Remez exchange: 2.6e-6, 2^-18).  Below 2^-126.5 and for -inf the result is 0.  NaN gives 0: the
+// caller makes every score of such a row NaN, and those that go through ex2 keep it.
+__device__ __forceinline__ void poly_exp2(uint64_t x, float& lo, float& hi) {
+  const uint64_t y = f32x2(fmaxf(f32x2_lo(x), -127.f), fmaxf(f32x2_hi(x), -127.f));
+  const uint64_t t = add2(y, f32x2(12583039.f, 12583039.f));
+  const uint64_t n = add2(t, f32x2(-12583039.f, -12583039.f));
+  const uint64_t r = fma2(n, f32x2(-1.f, -1.f), y);
+  uint64_t q = fma2(r, f32x2(0.009570102207362652f, 0.009570102207362652f), f32x2(0.05591785907745361f, 0.05591785907745361f));
+  q = fma2(q, r, f32x2(0.240247443318367f, 0.240247443318367f));
+  q = fma2(q, r, f32x2(0.6931217908859253f, 0.6931217908859253f));
+  q = fma2(q, r, f32x2(0.9999992847442627f, 0.9999992847442627f));
+  q = mul2(q, f32x2(__uint_as_float(static_cast<uint32_t>(t) << 23), __uint_as_float(static_cast<uint32_t>(t >> 32) << 23)));
+  lo = f32x2_lo(q);
+  hi = f32x2_hi(q);
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  constexpr int NT = C::NT, SB = C::SB, CK = C::CK, HALVES = C::HALVES, BLK = C::BLK, D = C::D;
-  constexpr int ST = C::STAGES;
+  constexpr int NT = C::NT, SB = C::SB, KT = C::KT, KC = C::KC, VC = C::VC, VK = C::VK, BLK = C::BLK, D = C::D;
+  constexpr int ST = C::STAGES, PH = C::PH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sq = smem;
   uint8_t* skv = smem + C::SMEM_Q;
   Bars<C>* b = reinterpret_cast<Bars<C>*>(skv + ST * C::CHUNK);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  static_assert(sizeof(Bars<C>) <= 1024, "barriers");
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be the same for the whole warp)
   const int TT = p.tile_tokens;
 
   if (tid == 0) {
     mbar_init(&b->q_full, 1);
-    mbar_init(&b->q_empty, 1);
+    mbar_init(&b->q_empty, NT);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&b->kv_full[i], 1);
-      mbar_init(&b->kv_empty[i], 3);  // the MMA commit and the two guard warps
-      mbar_init(&b->v_ready[i], 64);
+      mbar_init(&b->kv_empty[i], NT);
+      mbar_init(&b->v_guard[i], 1);
+      mbar_init(&b->v_ready[i], 1);
     }
     for (int i = 0; i < NT * SB; ++i) {
       mbar_init(&b->s_full[i], 1);
-      mbar_init(&b->p_full[i], 128);
-    }
-    for (int i = 0; i < NT; ++i) {
+      for (int h = 0; h < C::PH; ++h) mbar_init(&b->p_full[i][h], 4);
       mbar_init(&b->o_done[i], 1);
-      mbar_init(&b->o_free[i], 128);
+    }
+    for (int i = 0; i < NT; ++i) mbar_init(&b->o_free[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b->next_full[i], 1);
+      mbar_init(&b->next_empty[i], C::WARPS);
     }
     b->abort = 0;
     for (int i = 0; i < kFlagSlots; ++i) b->bad[i] = -1;
     mbar_fence_init();
   }
-  if (warp == C::SOFT_WARPS) {
+  if (warp == C::PRODUCER) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(&b->tmem))
                  : "memory");
@@ -177,298 +272,369 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = b->tmem;
-  const int64_t first = blockIdx.x, step = gridDim.x;
+  // (all 512 columns of tensor memory are this CTA's: they start at column 0)
 
-  if (warp == C::SOFT_WARPS) {
+  if (warp == C::PRODUCER) {
     // ---------------------------------------------------------------- producer
     if (lane == 0) {
-      uint32_t ring = 0;  // chunks loaded so far
-      int n_item = 0;
-      bool go = true;
-      Item it;
-      for (int64_t idx = first; go && get_item(p, NT, idx, it); idx += step, ++n_item) {
-        int n = 0, tiles = 0;
-        for (int t = 0; t < NT; ++t) {
-          const int nt = key_tiles(it, t, TT);
-          n = max(n, nt);
-          tiles += nt > 0;
-        }
-        if (n_item > 0 && !wait_bar(&b->q_empty, (n_item - 1) & 1, b, p.status)) break;
+    Ring<ST> ring;  // the next chunk to load
+    int n_item = 0, asked = 0;
+    bool go = true;
+    // the item after next is asked for when every role has taken the one before it
+    auto ask = [&] {
+      const int s = asked & 1;
+      if (asked >= 2 && !wait_bar(&b->next_empty[s], ((asked >> 1) - 1) & 1, b, p.status)) return false;
+      {
+        mbar_arrive_expect_tx(&b->next_full[s], 16);
+        clc_request(&b->next[s], &b->next_full[s]);
+      }
+      ++asked;
+      return true;
+    };
+    ask();
+    for (;;) {
+      const int64_t idx = next_item<true>(n_item, b, p.status);
+      if (idx < 0) break;
+      if (n_item > 0 && !ask()) break;
+      const Item it = get_item(p, NT, idx);
+      int n = 0, tiles = 0;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int nt = key_steps<C>(it, t, TT);
+        n = max(n, nt);
+        tiles += nt > 0;
+      }
+      if (n_item > 0 && !wait_bar(&b->q_empty, (n_item - 1) & 1, b, p.status)) break;
+      ++n_item;
+      {
         mbar_arrive_expect_tx(&b->q_full, tiles * BLK * TT * p.g * 128);
         for (int t = 0; t < tiles; ++t)
           for (int k = 0; k < BLK; ++k)
             tma_load_4d(sq + t * C::Q_TILE + k * C::Q_BLOCK, &qmap, 64 * k, 0, it.h,
                         it.row0 + it.t0 + t * TT, &b->q_full);
-        auto load = [&](const CUtensorMap* map, int key) {
-          const int s = ring % ST;
-          if (ring >= ST && !wait_bar(&b->kv_empty[s], (ring / ST - 1) & 1, b, p.status)) return false;
-          mbar_arrive_expect_tx(&b->kv_full[s], C::CHUNK);
-          for (int k = 0; k < BLK; ++k)
-            tma_load_3d(skv + s * C::CHUNK + k * C::KV_BLOCK, map, 64 * k, it.h, it.row0 + key,
-                        &b->kv_full[s]);
-          ++ring;
-          return true;
-        };
-        for (int j = -SB; go && j < n; ++j) {  // V of tile j, then K of tile j + SB
-          for (int f = 0; go && f < HALVES && j >= 0; ++f) go = load(&vmap, 128 * j + CK * f);
-          for (int f = 0; go && f < HALVES && j + SB < n; ++f) go = load(&kmap, 128 * (j + SB) + CK * f);
+      }
+      auto slot = [&] {  // waits until the ring's next chunk is free
+        return ring.round == 0 || wait_bar(&b->kv_empty[ring.stage], (ring.round - 1) & 1, b, p.status);
+      };
+      for (int j = -SB; go && j < n; ++j) {  // V of step j, then K of step j + SB
+        if (j >= 0) {
+#pragma unroll
+          for (int f = 0; f < VC; ++f) {
+            if (!(go = go && slot())) break;
+            {
+              uint64_t* bar = &b->kv_full[ring.stage];
+              mbar_arrive_expect_tx(bar, C::CHUNK);
+#pragma unroll
+              for (int k = 0; k < BLK; ++k)
+                tma_load_3d(skv + ring.stage * C::CHUNK + k * C::V_BLOCK, &vmap, 64 * k, it.h,
+                            it.row0 + KT * j + VK * f, bar);
+              if (guarded<C>(it, KT * j + VK * f)) mbar_arrive(&b->v_guard[ring.stage]);
+            }
+            ring.step();
+          }
+        }
+        if (j + SB < n) {
+#pragma unroll
+          for (int f = 0; f < KC; ++f) {
+            if (!(go = go && slot())) break;
+            {
+              uint64_t* bar = &b->kv_full[ring.stage];
+              mbar_arrive_expect_tx(bar, C::CHUNK);
+#pragma unroll
+              for (int k = 0; k < C::KB; ++k)
+                tma_load_3d(skv + ring.stage * C::CHUNK + k * C::K_BLOCK, &kmap, 64 * (C::KB * f + k), it.h,
+                            it.row0 + KT * (j + SB), bar);
+            }
+            ring.step();
+          }
         }
       }
-      // every copy has landed and every chunk was consumed before the CTA ends
+      if (!go) break;
+    }
+    // every copy and answer has landed and every chunk was consumed before the CTA ends
+    {
       const uint64_t limit = *reinterpret_cast<volatile int32_t*>(&b->abort) ? 100000000ull : 2000000000ull;
-      for (uint32_t r = ring > ST ? ring - ST : 0; r < ring; ++r) {
-        mbar_wait(&b->kv_full[r % ST], (r / ST) & 1, limit);
-        mbar_wait(&b->kv_empty[r % ST], (r / ST) & 1, limit);
+      for (uint32_t s = 0; s < ST; ++s) {  // each stage's last round
+        const uint32_t rounds = ring.round + (s < ring.stage ? 1 : 0);
+        if (rounds == 0) continue;
+        mbar_wait(&b->kv_full[s], (rounds - 1) & 1, limit);
+        mbar_wait(&b->kv_empty[s], (rounds - 1) & 1, limit);
       }
       if (n_item > 0) mbar_wait(&b->q_empty, (n_item - 1) & 1, limit);
+      mbar_wait(&b->next_full[(asked - 1) & 1], ((asked - 1) >> 1) & 1, limit);
+    }
     }
     __syncwarp();
-  } else if (warp == C::SOFT_WARPS + 1) {
-    // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      uint32_t ring = 0, v_phase = 0;         // chunks consumed; phases of v_ready, a bit a stage
-      uint32_t n_p[NT * SB] = {};             // probability tiles consumed per buffer
-      uint32_t n_out[NT] = {};                // items that had tile t so far
-      int n_item = 0;
-      bool go = true;
-      Item it;
-      for (int64_t idx = first; go && get_item(p, NT, idx, it); idx += step, ++n_item) {
-        int n[NT], nmax = 0;
-        for (int t = 0; t < NT; ++t) nmax = max(nmax, n[t] = key_tiles(it, t, TT));
-        auto wait_k = [&](uint32_t r) {
-          return wait_bar(&b->kv_full[r % ST], (r / ST) & 1, b, p.status);
-        };
-        auto wait_v = [&](uint32_t r, int key) {
-          const uint32_t s = r % ST;
-          if (!guarded<C>(it, key)) return wait_k(r);
-          const bool ok = wait_bar(&b->v_ready[s], (v_phase >> s) & 1, b, p.status);
-          v_phase ^= 1u << s;
-          return ok;
-        };
-        // S[t] (buffer sb) = Q[t] K^T for the CK keys of ring chunk r, columns CK * f on
-        auto scores = [&](int t, int sb, int f, uint32_t r) {
-          const uint32_t qa = smem_addr(sq + t * C::Q_TILE);
-          const uint32_t ka = smem_addr(skv + (r % ST) * C::CHUNK);
-          const uint32_t d = tmem + (t * SB + sb) * 128 + CK * f;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc_mma_ss(d, tc_smem_desc(qa + (k / 4) * C::Q_BLOCK + (k % 4) * 32, 16, 1024),
-                      tc_smem_desc(ka + (k / 4) * C::KV_BLOCK + (k % 4) * 32, 16, 1024), C::IDESC_S, k > 0);
-        };
-        // O[t] (+)= P[t] V for the CK keys of ring chunk r
-        auto values = [&](int t, int sb, int f, uint32_t r, bool acc) {
-          const uint32_t va = smem_addr(skv + (r % ST) * C::CHUNK);
-          const uint32_t pa = tmem + (t * SB + sb) * 128 + (CK / 2) * f;
-#pragma unroll
-          for (int k = 0; k < CK / 16; ++k)
-            tc_mma_ts(tmem + kOutCol + t * D, pa + 8 * k, tc_smem_desc(va + 2048 * k, C::KV_BLOCK, 1024),
-                      C::IDESC_PV, acc || k > 0);
-        };
-        go = wait_bar(&b->q_full, n_item & 1, b, p.status);
-        for (int j = 0; go && j < SB && j < nmax; ++j) {  // the first score tiles
-          for (int f = 0; go && f < HALVES; ++f) {
-            if (!(go = wait_k(ring))) break;
-            for (int t = 0; t < NT; ++t)
-              if (j < n[t]) {
-                scores(t, j, f, ring);
-                if (f + 1 == HALVES) tc_commit(&b->s_full[t * SB + j]);
-              }
-            tc_commit(&b->kv_empty[ring % ST]);
-            ++ring;
-          }
-        }
-        if (go && nmax <= SB) tc_commit(&b->q_empty);
-        for (int j = 0; go && j < nmax; ++j) {
-          const int sb = j % SB;
-          const uint32_t rv = ring, rk = ring + HALVES;  // chunks of V tile j and K tile j + SB
-          const bool more = j + SB < nmax;
-          bool have_v = false, have_k = false;
-          for (int t = 0; go && t < NT; ++t) {
-            if (j >= n[t]) continue;
-            const int buf = t * SB + sb;
-            if (j == 0 && n_out[t]++ > 0 && !(go = wait_bar(&b->o_free[t], n_out[t] & 1, b, p.status))) break;
-            if (!(go = wait_bar(&b->p_full[buf], n_p[buf]++ & 1, b, p.status))) break;
-            tc_fence_after();
-            for (int f = 0; f < HALVES; ++f) {
-              if (!have_v && !(go = wait_v(rv + f, 128 * j + CK * f))) break;
-              tc_fence_after();
-              values(t, sb, f, rv + f, j > 0 || f > 0);
-            }
-            if (!go) break;
-            have_v = true;
-            tc_commit(&b->o_done[t]);
-            if (t == NT - 1 || j >= n[NT - 1])
-              for (int f = 0; f < HALVES; ++f) tc_commit(&b->kv_empty[(rv + f) % ST]);
-            if (j + SB < n[t]) {
-              for (int f = 0; f < HALVES; ++f) {
-                if (!have_k && !(go = wait_k(rk + f))) break;
-                scores(t, sb, f, rk + f);
-              }
-              if (!go) break;
-              have_k = true;
-              tc_commit(&b->s_full[buf]);
-            }
-            if (more && (t == NT - 1 || j >= n[NT - 1]))
-              for (int f = 0; f < HALVES; ++f) tc_commit(&b->kv_empty[(rk + f) % ST]);
-          }
-          if (go && j + SB + 1 == nmax) tc_commit(&b->q_empty);  // the item's last scores are issued
-          ring += HALVES + (more ? HALVES : 0);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp >= C::SOFT_WARPS + 2) {
-    // ---------------------------------------------------------------- guard
-    // (follows every chunk, so that the parity it waits for is never more than a phase away)
-    const int gtid = tid - 32 * (C::SOFT_WARPS + 2);
-    uint32_t ring = 0;
-    int n_item = 0;
+  } else if (warp >= C::MMA) {
+    // ---------------------------------------------------------------- MMA, one warp per tile
+    // Per step: O (+)= P V of step j, then S = Q K^T of step j + SB.  The tensor core's queue holds a
+    // few MMAs only, so what a warp spends on looking at barriers between them would be lost; with a
+    // warp per tile it passes while the other tile's MMAs run.  (A warp runs as a whole and one lane
+    // issues: control flow and operands are then known to be uniform, as the MMAs' operands have to
+    // be.  It walks over every chunk of the item, also those that only the other tile needs.)
+    const int t = warp - C::MMA;
+    Ring<ST> ring;                          // the next chunk
+    uint32_t v_phase = 0;                   // phases of v_ready, a bit a stage
+    uint32_t p_phase = 0;                   // phases of p_full, a bit a buffer of the tile
+    uint32_t n_out = 0;                     // items that had this tile so far
+    const uint32_t lead = elect_lane() ? 1u : 0u;
+    // start addresses of the operands' descriptors, in units of 16 bytes
+    const uint32_t q16 = (smem_addr(sq) + t * C::Q_TILE) >> 4, kv16 = smem_addr(skv) >> 4;
+    const uint32_t o = kOutCol + t * D;
     bool go = true;
-    Item it;
-    for (int64_t idx = first; go && get_item(p, NT, idx, it); idx += step, ++n_item) {
-      int n = 0;
-      for (int t = 0; t < NT; ++t) n = max(n, key_tiles(it, t, TT));
-      // one chunk: K, or V with first key c0
-      auto chunk = [&](bool value, int c0) {
-        const int s = ring % ST;
-        if (!__all_sync(0xffffffffu, wait_bar(&b->kv_full[s], (ring / ST) & 1, b, p.status))) return false;
-        if (value && guarded<C>(it, c0)) {
-          uint4* v = reinterpret_cast<uint4*>(skv + s * C::CHUNK);
-          bool found = false;
-          for (int i = gtid; i < C::CHUNK / 16; i += 64) {  // 16 bytes of one key's row
-            const int key = c0 + (i / 8) % CK;
-            if (key >= it.len) {
-              v[i] = make_uint4(0, 0, 0, 0);
-            } else {
-              const uint4 x = v[i];
-              if (nonfinite8(x)) {
-                v[i] = make_uint4(zero_nonfinite(x.x), zero_nonfinite(x.y), zero_nonfinite(x.z), zero_nonfinite(x.w));
-                found = true;
-              }
-            }
-          }
-          if (found) *reinterpret_cast<volatile int32_t*>(&b->bad[n_item % kFlagSlots]) = n_item;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // these stores -> tensor core
-          mbar_arrive(&b->v_ready[s]);
+    for (int n_item = 0; go; ++n_item) {
+      const int64_t idx = next_item<false>(n_item, b, p.status);
+      if (idx < 0) break;
+      const Item it = get_item(p, NT, idx);
+      const int n = key_steps<C>(it, t, TT);
+      const int nmax = NT == 1 ? n : max(n, key_steps<C>(it, 1 - t, TT));
+      if (!(go = wait_spin(&b->q_full, n_item & 1, b, p.status))) break;
+      if (n > 0 && n_out++ > 0 && !(go = wait_spin(&b->o_free[t], n_out & 1, b, p.status))) break;
+#pragma unroll 1
+      for (int j = -SB; go && j < nmax; ++j) {
+        const int sb = j & 1, buf = t * SB + sb;
+        const bool do_v = j >= 0, do_k = j + SB < nmax;
+        const bool pv = do_v && j < n, qk = do_k && j + SB < n;
+        const Ring<ST> rv = ring, rk = do_v ? ring.plus(VC) : ring;  // V chunks of step j, K of j + SB
+        const uint32_t p_par = (p_phase >> sb) & 1;
+        // barriers of the chunks: V through the guard where the causal line or the prompt's end cross
+        uint64_t *v_bar[VC], *k_bar[KC];
+        uint32_t v_par[VC], k_par[KC];
+#pragma unroll
+        for (int f = 0; f < VC; ++f) {
+          const Ring<ST> r = rv.plus(f);
+          const bool guard = do_v && guarded<C>(it, KT * j + VK * f);
+          v_bar[f] = guard ? &b->v_ready[r.stage] : &b->kv_full[r.stage];
+          v_par[f] = guard ? (v_phase >> r.stage) & 1 : r.round & 1;
+          if (guard) v_phase ^= 1u << r.stage;
         }
-        if (lane == 0) mbar_arrive(&b->kv_empty[s]);
-        ++ring;
+#pragma unroll
+        for (int f = 0; f < KC; ++f) {
+          const Ring<ST> r = rk.plus(f);
+          k_bar[f] = &b->kv_full[r.stage];
+          k_par[f] = r.round & 1;
+        }
+        // One look at all barriers of a step together costs a third of looking at one after the other
+        // (about 130 cycles each); only what is not there yet is waited for below.
+        bool ready = false;
+        if (pv && qk) {
+          bool all = true;
+#pragma unroll
+          for (int h = 0; h < PH; ++h) all &= mbar_try_wait(&b->p_full[buf][h], p_par);
+#pragma unroll
+          for (int f = 0; f < VC; ++f) all &= mbar_try_wait(v_bar[f], v_par[f]);
+#pragma unroll
+          for (int f = 0; f < KC; ++f) all &= mbar_try_wait(k_bar[f], k_par[f]);
+          ready = __all_sync(0xffffffffu, all);
+        }
+        if (pv) {
+#pragma unroll
+          for (int h = 0; h < PH; ++h) {  // 64 keys at a time, as the probabilities come
+            constexpr int kPerChunk = C::VK / 64;
+            const Ring<ST> r = rv.plus(h / kPerChunk);
+            if (!ready) {
+              if (h % kPerChunk == 0) go = go && wait_spin(v_bar[h / kPerChunk], v_par[h / kPerChunk], b, p.status);
+              go = go && wait_spin(&b->p_full[buf][h], p_par, b, p.status);
+              if (!go) break;
+            }
+            tc_fence_after();
+            const uint32_t vd = kv16 + r.stage * (C::CHUNK / 16) + (h % kPerChunk) * (64 * 128 / 16);
+            const uint32_t pa = buf * KT + 32 * h;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma_ts(lead, o, pa + 8 * k, vd + (2048 / 16) * k, kDescV<C>, C::IDESC_PV, h > 0 || k > 0 || j > 0);
+            if ((h + 1) % kPerChunk == 0) tc_commit(lead, &b->kv_empty[r.stage]);
+          }
+          if (!go) break;
+          tc_commit(lead, &b->o_done[buf]);
+          p_phase ^= 1u << sb;
+        } else if (do_v) {  // chunks that only the other tile uses
+#pragma unroll
+          for (int f = 0; f < VC; ++f) {
+            if (!(go = go && wait_spin(v_bar[f], v_par[f], b, p.status))) break;
+            if (lead) mbar_arrive(&b->kv_empty[rv.plus(f).stage]);
+          }
+        }
+        if (qk) {
+#pragma unroll
+          for (int f = 0; f < KC; ++f) {
+            const Ring<ST> r = rk.plus(f);
+            if (!ready && !(go = wait_spin(k_bar[f], k_par[f], b, p.status))) break;
+            tc_fence_after();
+            const uint32_t qd = q16 + f * C::KB * C::Q_BLOCK / 16;
+            const uint32_t kd = kv16 + r.stage * (C::CHUNK / 16);
+#pragma unroll
+            for (int k = 0; k < 4 * C::KB; ++k)
+              tc_mma_ss(lead, buf * KT, qd + ((k / 4) * C::Q_BLOCK + (k % 4) * 32) / 16,
+                        kd + ((k / 4) * C::K_BLOCK + (k % 4) * 32) / 16, kDescK, C::IDESC_S, f > 0 || k > 0);
+            if (f + 1 == KC) tc_commit(lead, &b->s_full[buf]);
+            tc_commit(lead, &b->kv_empty[r.stage]);
+          }
+          if (j + SB + 1 == n) tc_commit(lead, &b->q_empty);  // this tile's last scores are issued
+        } else if (do_k) {
+#pragma unroll
+          for (int f = 0; f < KC; ++f) {
+            if (!(go = go && wait_spin(k_bar[f], k_par[f], b, p.status))) break;
+            if (lead) mbar_arrive(&b->kv_empty[rk.plus(f).stage]);
+          }
+        }
+        ring = do_k ? rk.plus(KC) : rk;
+      }
+      if (go && n == 0 && lead) mbar_arrive(&b->q_empty);
+    }
+    __syncwarp();
+  } else if (warp == C::GUARD) {
+    // ---------------------------------------------------------------- guard
+    // (The producer tells it of a chunk's load, per stage, so that the parities it waits for are
+    // never more than a phase away.)
+    Ring<ST> ring;
+    uint32_t g_phase = 0;  // phases of v_guard, a bit a stage
+    bool go = true;
+    for (int n_item = 0; go; ++n_item) {
+      const int64_t idx = next_item<false>(n_item, b, p.status);
+      if (idx < 0) break;
+      const Item it = get_item(p, NT, idx);
+      int n = 0;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) n = max(n, key_steps<C>(it, t, TT));
+      auto scan = [&](int c0) {  // the chunk at the ring's position, with first key c0
+        const int s = ring.stage;
+        if (!wait_bar_warp(&b->v_guard[s], (g_phase >> s) & 1, b, p.status)) return false;
+        g_phase ^= 1u << s;
+        if (!wait_bar_warp(&b->kv_full[s], ring.round & 1, b, p.status)) return false;
+        uint4* v = reinterpret_cast<uint4*>(skv + s * C::CHUNK);
+        bool found = false;
+#pragma unroll 4
+        for (int i = lane; i < C::CHUNK / 16; i += 32) {  // 16 bytes of one key's row
+          const int key = c0 + (i / 8) % VK;
+          const uint4 x = v[i];
+          if (key >= it.len) {
+            v[i] = make_uint4(0, 0, 0, 0);
+          } else if (nonfinite8(x)) {
+            v[i] = make_uint4(zero_nonfinite(x.x), zero_nonfinite(x.y), zero_nonfinite(x.z), zero_nonfinite(x.w));
+            found = true;
+          }
+        }
+        if (found) *reinterpret_cast<volatile int32_t*>(&b->bad[n_item % kFlagSlots]) = n_item;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // these stores -> tensor core
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b->v_ready[s]);
         return true;
       };
+#pragma unroll 1
       for (int j = -SB; go && j < n; ++j) {
-        for (int f = 0; go && f < HALVES && j >= 0; ++f) go = chunk(true, 128 * j + CK * f);
-        for (int f = 0; go && f < HALVES && j + SB < n; ++f) go = chunk(false, 0);
+        for (int f = 0; go && f < VC && j >= 0; ++f, ring.step())
+          if (guarded<C>(it, KT * j + VK * f)) go = scan(KT * j + VK * f);
+        for (int f = 0; f < KC && j + SB < n; ++f) ring.step();
       }
     }
   } else {
     // ---------------------------------------------------------------- softmax and output
     const int t = warp / 4, r = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t o_addr = tmem + lane_base + kOutCol + t * D;
+    const uint32_t o_addr = lane_base + kOutCol + t * D;
     const int tok = min(r / p.g, TT - 1), gi = r - (r / p.g) * p.g;
     const float c = p.c;
     const uint64_t c2 = f32x2(c, c);
-    uint32_t n_s[SB] = {}, n_o = 0;  // score tiles per buffer, P V products of this tile so far
-    int n_item = 0;
+    uint32_t phase = 0;   // phases of this tile's score buffers, a bit a buffer
     bool go = true;
-    Item it;
-    for (int64_t idx = first; go && get_item(p, NT, idx, it); idx += step, ++n_item) {
-      const int n = key_tiles(it, t, TT);
+    for (int n_item = 0; go; ++n_item) {
+      const int64_t idx = next_item<false>(n_item, b, p.status);
+      if (idx < 0) break;
+      const Item it = get_item(p, NT, idx);
+      const int n = key_steps<C>(it, t, TT);
+      if (n == 0) continue;
       const int pos = it.t0 + t * TT + tok;
       const bool mine = r < TT * p.g && pos < it.len;
-      float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j) {
-        const int sb = SB == 1 ? 0 : j & 1;
-        const int buf = t * SB + sb;
-        if (!(go = __all_sync(0xffffffffu, wait_bar(&b->s_full[buf], n_s[sb]++ & 1, b, p.status)))) break;
+      float m = -INFINITY;
+      uint64_t l2 = 0;
+      // Waits for the product of step j.  (The scores of step j + 1 are there, so the product of step
+      // j - 1 is done: the parity of this buffer's barrier is at most a phase away.)
+      auto wait_product = [&](int j) {
+        const int sb = j & 1;
+        const bool ok = wait_bar_warp(&b->o_done[t * SB + sb], (~phase >> sb) & 1, b, p.status);
         tc_fence_after();
-        const uint32_t s_addr = tmem + lane_base + buf * 128;
-        const int vis = pos + 1 - 128 * j;  // visible columns of this row (>= 128: all)
-        const bool masked = __any_sync(0xffffffffu, vis < 128);
-        uint32_t x[32], y[32];
-        float mx = -INFINITY;
-        tmem_ld32(x, s_addr);
-        tmem_wait_ld(x);
+        return ok;
+      };
+      for (int j = 0; j < n; ++j) {
+        const int sb = j & 1, buf = t * SB + sb;
+        if (!(go = wait_bar_warp(&b->s_full[buf], (phase >> sb) & 1, b, p.status))) break;
+        tc_fence_after();
+        const uint32_t s_addr = lane_base + buf * KT;
+        uint32_t x[KT / 32][32];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t(&cur)[32] = k & 1 ? y : x;
-          uint32_t(&nxt)[32] = k & 1 ? x : y;
-          if (k < 3) tmem_ld32(nxt, s_addr + 32 * (k + 1));
-          if (masked) {
+        for (int k = 0; k < KT / 32; ++k) tmem_ld32(x[k], s_addr + 32 * k);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              mx = fmaxf(mx, 32 * k + i < vis ? __uint_as_float(cur[i]) : -INFINITY);
-          } else {
+        for (int k = 0; k < KT / 32; ++k) tmem_wait_ld(x[k]);
+        const int vis = pos + 1 - KT * j;  // visible columns of this row (>= KT: all)
+        if (__any_sync(0xffffffffu, vis < KT)) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              mx = fmaxf(mx, fmaxf(__uint_as_float(cur[i]), __uint_as_float(cur[i + 1])));
-          }
-          if (k < 3) tmem_wait_ld(nxt);
+          for (int i = 0; i < KT; ++i)
+            if (i >= vis) x[i / 32][i % 32] = 0xff800000u;  // -inf
         }
-        const bool up = (mx - m) * c > kRescaleAbove;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < KT / 2; ++i)
+          mx[i % 4] = max3_nan(mx[i % 4], __uint_as_float(x[i / 16][2 * (i % 16)]),
+                               __uint_as_float(x[i / 16][2 * (i % 16) + 1]));
+        float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+        // a visible score that is NaN or +inf makes the whole row NaN, as in the formula
+        if (!(top < INFINITY)) m = top = __uint_as_float(0x7fc00000u);
+        const bool up = (top - m) * c > kRescaleAbove;
         if (j == 0) {
-          m = mx;
+          m = top;
         } else if (__any_sync(0xffffffffu, up)) {
-          const float mn = up ? mx : m;
+          const float mn = up ? top : m;
           const float a = up ? fast_exp2((m - mn) * c) : 1.f;
           m = mn;
-          l *= a;
-          if (!(go = __all_sync(0xffffffffu, wait_bar(&b->o_done[t], (n_o - 1) & 1, b, p.status)))) break;
-          tc_fence_after();
+          l2 = mul2(l2, f32x2(a, a));
+          if (!(go = wait_product(j - 1))) break;
 #pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            tmem_ld32(x, o_addr + 32 * k);
-            tmem_wait_ld(x);
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t o[16];
+            tmem_ld16(o, o_addr + 16 * k);
+            tmem_wait_ld(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * a);
-            tmem_st32(o_addr + 32 * k, x);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+            tmem_st16(o_addr + 16 * k, o);
           }
         }
         const float mc = m == -INFINITY ? 0.f : m * c;
         const uint64_t mc2 = f32x2(-mc, -mc);
-        uint64_t l2 = 0;
-        tmem_ld32(x, s_addr);
-        tmem_wait_ld(x);
+        uint64_t la = 0, lb = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t(&cur)[32] = k & 1 ? y : x;
-          uint32_t(&nxt)[32] = k & 1 ? x : y;
-          if (k < 3) tmem_ld32(nxt, s_addr + 32 * (k + 1));
-          uint32_t pk[16];
+        for (int h = 0; h < PH; ++h) {
+          uint32_t pk[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t z = fma2(f32x2(__uint_as_float(cur[2 * i]), __uint_as_float(cur[2 * i + 1])), c2, mc2);
-            float p0 = fast_exp2(f32x2_lo(z)), p1 = fast_exp2(f32x2_hi(z));
-            if (masked) {
-              if (32 * k + 2 * i >= vis) p0 = 0.f;
-              if (32 * k + 2 * i + 1 >= vis) p1 = 0.f;
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t(&xs)[32] = x[2 * h + i / 16];
+            const uint64_t z =
+                fma2(f32x2(__uint_as_float(xs[2 * (i % 16)]), __uint_as_float(xs[2 * (i % 16) + 1])), c2, mc2);
+            float p0, p1;
+            if (i % 16 < C::POLY) {
+              poly_exp2(z, p0, p1);
+            } else {
+              p0 = fast_exp2(f32x2_lo(z));
+              p1 = fast_exp2(f32x2_hi(z));
             }
-            l2 = add2(l2, f32x2(p0, p1));
+            uint64_t& l = i % 2 ? lb : la;
+            l = add2(l, f32x2(p0, p1));
             pk[i] = pack_bf16x2(p0, p1);
           }
-          if (k < 3) tmem_wait_ld(nxt);
-          tmem_st16(s_addr + 16 * k, pk);  // columns whose scores were read already
+          tmem_st32(s_addr + 32 * h, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b->p_full[buf][h]);
         }
-        l += f32x2_lo(l2) + f32x2_hi(l2);
-        // With two score buffers this tile may be done before the last tile's product; the next
-        // scores follow that product, so waiting for it here costs nothing and keeps the parity
-        // that the waits on o_done use no more than a phase away.
-        if (SB > 1 && j > 0 &&
-            !(go = __all_sync(0xffffffffu, wait_bar(&b->o_done[t], (n_o - 1) & 1, b, p.status))))
-          break;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&b->p_full[buf]);
-        ++n_o;
+        l2 = add2(l2, add2(la, lb));
+        phase ^= 1u << sb;
       }
       if (!go) break;
-      if (n == 0) continue;  // (o_free[t] counts the items that have this tile)
       // ---- output
-      if (!(go = __all_sync(0xffffffffu, wait_bar(&b->o_done[t], (n_o - 1) & 1, b, p.status)))) break;
-      tc_fence_after();
-      const float inv = 1.f / l;
+      if (!(go = wait_product(n - 1))) break;
+      // (a row whose scores are all -inf has no weights: NaN, as in the formula)
+      const float inv = m == -INFINITY ? __uint_as_float(0x7fc00000u) : 1.f / (f32x2_lo(l2) + f32x2_hi(l2));
       const bool bad = *reinterpret_cast<volatile int32_t*>(&b->bad[n_item % kFlagSlots]) == n_item;
       uint16_t* out = p.out + (static_cast<int64_t>(it.row0 + pos) * p.Hq + it.h * p.g + gi) * D;
 #pragma unroll 1
@@ -476,17 +642,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         uint32_t x[32];
         tmem_ld32(x, o_addr + 32 * k);
         tmem_wait_ld(x);
-        if (mine && bad) {  // non-finite V elements that this row sees, on the chunks the guard cleaned
-          const int e0 = (it.t0 + 1) / CK * CK;
-#pragma unroll 1
-          for (int key = e0; key <= pos; ++key) {
-            const uint16_t* v = p.v + static_cast<int64_t>(it.row0 + key) * p.v_stride + it.h * D + 32 * k;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if ((v[i] & 0x7f80u) == 0x7f80u)
-                x[i] = __float_as_uint(__uint_as_float(x[i]) + bf16_bits_to_float(v[i]));
-          }
-        }
         if (mine) {
           uint4* o4 = reinterpret_cast<uint4*>(out + 32 * k);
 #pragma unroll
@@ -501,7 +656,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
       }
       tc_fence_before();
-      mbar_arrive(&b->o_free[t]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->o_free[t]);
+      if (mine && bad) {  // non-finite V elements that this row sees, of the chunks that the guard cleaned
+#pragma unroll 1
+        for (int key = (it.t0 + 1) / VK * VK; key <= pos; ++key) {
+          const uint16_t* v = p.v + static_cast<int64_t>(it.row0 + key) * p.v_stride + it.h * D;
+#pragma unroll 1
+          for (int i = 0; i < D; ++i)
+            if ((v[i] & 0x7f80u) == 0x7f80u)
+              out[i] = static_cast<uint16_t>(pack_bf16x2(bf16_bits_to_float(out[i]) + bf16_bits_to_float(v[i]), 0.f));
+        }
+      }
     }
   }
   __syncthreads();
@@ -512,9 +678,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     __syncthreads();
   }
-  if (warp == C::SOFT_WARPS) {
+  if (warp == C::PRODUCER) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(b->tmem) : "memory");
   }
 }
 
@@ -568,8 +734,9 @@ cudaError_t launch_prompt(const PromptParams& p, const PromptInputs& in, cudaStr
   const cuuint64_t qd[4] = {D, g, Hkv, rows}, qs[3] = {2 * D, 2 * g * D, 2ull * in.q_stride};
   const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(p.g), 1, static_cast<cuuint32_t>(p.tile_tokens)};
   const cuuint64_t kd[3] = {D, Hkv, rows}, ks[2] = {2 * D, 2ull * in.k_stride}, vs[2] = {2 * D, 2ull * in.v_stride};
-  const cuuint32_t kb[3] = {64, 1, static_cast<cuuint32_t>(p.D == 256 ? Cfg<256>::CK : Cfg<128>::CK)};
-  if (!make_map(&q, in.q, 4, qd, qs, qb) || !make_map(&k, in.k, 3, kd, ks, kb) || !make_map(&v, in.v, 3, kd, vs, kb))
+  const cuuint32_t kb[3] = {64, 1, static_cast<cuuint32_t>(p.D == 256 ? Cfg<256>::KT : Cfg<128>::KT)};
+  const cuuint32_t vb[3] = {64, 1, 64};
+  if (!make_map(&q, in.q, 4, qd, qs, qb) || !make_map(&k, in.k, 3, kd, ks, kb) || !make_map(&v, in.v, 3, kd, vs, vb))
     return cudaErrorInvalidValue;
   return p.D == 64 ? launch<64>(p, q, k, v, s) : p.D == 128 ? launch<128>(p, q, k, v, s) : launch<256>(p, q, k, v, s);
 }

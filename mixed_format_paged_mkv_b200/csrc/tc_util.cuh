@@ -8,6 +8,15 @@
 
 namespace mkv {
 
+// One lane of a converged warp: true on it alone.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // ------------------------------------------------------------------ tensor-map loads
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
                                             uint64_t* bar) {
@@ -33,28 +42,33 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// The barrier gets one arrival when every tcgen05 operation this thread issued so far is done.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_addr(bar))
-               : "memory");
-}
-// D (TMEM, fp32) (+)= A (shared memory) . B (shared memory), 16-bit operands, K = 16.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          bool accumulate) {
+// The operations below are run by a whole warp and issued by the lane whose `lead` is not 0 (always
+// the same one: operations of one thread are in order).
+// The barrier gets one arrival when every tcgen05 operation issued so far is done.
+__device__ __forceinline__ void tc_commit(uint32_t lead, uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(lead)
+      : "memory");
+}
+// D (TMEM, fp32) (+)= A (shared memory) . B (shared memory), 16-bit operands, K = 16.  a and b: start
+// addresses in units of 16 bytes (below 2^14), desc the rest of their descriptors.
+__device__ __forceinline__ void tc_mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint64_t desc,
+                                          uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(desc | a), "l"(desc | b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lead)
       : "memory");
 }
 // The same with A in TMEM (lane = row, a 32-bit column = two consecutive K elements).
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                          bool accumulate) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint64_t desc,
+                                          uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(desc | b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lead)
       : "memory");
 }
 // Instruction descriptor: D fp32 (bits 4-5), A and B bf16 (bits 7-9, 10-12), B's major dimension
@@ -67,7 +81,7 @@ constexpr uint32_t tc_idesc_bf16(int M, int N, bool b_n_major) {
 // that swizzle writes: rows of 128 bytes, 8 rows (1024 B) per swizzle atom.  stride: bytes from
 // one group of 8 rows to the next; lead: bytes between 64-element blocks along the rows'
 // direction (operands whose rows run along M or N only).  Version 1 at bit 46, swizzle 2 at 61.
-__device__ __forceinline__ uint64_t tc_smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+constexpr uint64_t tc_smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFF) |
          (static_cast<uint64_t>((lead >> 4) & 0x3FFF) << 16) |
          (static_cast<uint64_t>((stride >> 4) & 0x3FFF) << 32) | (1ull << 46) | (2ull << 61);
@@ -95,6 +109,17 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                :
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : MKV_R8(r, 0), MKV_R8(r, 8)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : MKV_RW8(r, 0), MKV_RW8(r, 8) : : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
@@ -115,6 +140,39 @@ __device__ __forceinline__ void tmem_wait_st() {
 #undef MKV_R8
 #undef MKV_I8
 #undef MKV_RW8
+
+// ------------------------------------------------------------------ work from CTAs not yet started
+// Ask the hardware for a CTA of this grid that has not started (it then never starts); the answer
+// (16 bytes) completes on the barrier, which must expect 16 bytes.
+__device__ __forceinline__ void clc_request(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(smem_addr(answer)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+// The x index of the CTA an answer names, -1: there was none left.
+__device__ __forceinline__ int64_t clc_answer(const void* answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return got ? static_cast<int64_t>(x) : -1;
+}
+
+// The largest of three; NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 // ------------------------------------------------------------------ pairs of fp32
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
