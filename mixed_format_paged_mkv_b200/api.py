@@ -54,15 +54,15 @@ SIGNATURES = {
                                                     ctypes.c_float, _P, _P]),
     "mkv_seq_reset": (ctypes.c_int, [_P, _I32, _P]),
     "mkv_seq_copy": (ctypes.c_int, [_P, _I32, _I32, _P]),
-    "mkv_seq_fork": (ctypes.c_int, [_P, _I32P, _I32P, _I32P, _I32, _P]),
-    "mkv_seq_truncate": (ctypes.c_int, [_P, _I32P, _I32P, _I32, _P]),
-    "mkv_seq_free": (ctypes.c_int, [_P, _I32P, _I32, _P]),
+    "mkv_seq_fork": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P]),
+    "mkv_seq_truncate": (ctypes.c_int, [_P, _P, _P, _I32, _P]),
+    "mkv_seq_free": (ctypes.c_int, [_P, _P, _I32, _P]),
     "mkv_pool_compact": (ctypes.c_int, [_P, _I32P, _P]),
     "mkv_materialise_kv": (ctypes.c_int, [_P, _I32, _P, _P, ctypes.c_int64, _P]),
     "mkv_prefill_kv": (ctypes.c_int, [_P, _I32P, _I32P, _I32, _P, _P, _I32, _P]),
-    "mkv_rope": (ctypes.c_int, [_P, _I64, _P, _I32, _P, _I32, _I32P, _I32, _P, _I64, _P, _I64, _I32,
+    "mkv_rope": (ctypes.c_int, [_P, _I64, _P, _I32, _P, _I32, _P, _I32, _P, _I64, _P, _I64, _I32,
                                 _P, _I64, _P, _I64, _P]),
-    "mkv_prompt_attention": (ctypes.c_int, [_P, _I32P, _I32, _P, _I64, _P, _I64, _P, _I64, _I32,
+    "mkv_prompt_attention": (ctypes.c_int, [_P, _P, _I32, _P, _I64, _P, _I64, _P, _I64, _I32,
                                             ctypes.c_float, _P, _P]),
     "mkv_selftest_wait": (ctypes.c_int, [_P, ctypes.c_int64, _P]),
     "mkv_selftest_tc_logits": (ctypes.c_int, [_P, _P, _P, _P, _P]),
@@ -137,21 +137,33 @@ def _dev_ptr(t, dtype, name):
 
 
 def _rows_ptr(t, heads, dim, name, device):
-    """Pointer and row stride (elements) of a bf16 [rows, heads, dim] tensor whose rows are
+    """Address, row stride (elements) and rows of a bf16 [rows, heads, dim] tensor whose rows are
     contiguous but may be further apart, such as a part of a fused projection's output."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the pool on {device}")
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the pool on cuda:{device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be [rows, {heads}, {dim}]")
-    if t.numel() and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)):
+    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != dim)):
         raise ValueError(f"{name}: each row must be contiguous")
-    stride = t.stride(0) if t.shape[0] > 1 else heads * dim
-    return ctypes.c_void_p(t.data_ptr()), stride
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * dim, shape[0]
+
+
+def _i32_list(xs):
+    """A host int32 array of a short list (cheaper than _i32_array's numpy for the list's sake) and
+    its length."""
+    if isinstance(xs, (list, tuple)):
+        try:
+            return (ctypes.c_int32 * len(xs))(*xs), len(xs)
+        except TypeError:  # numpy integers and the like
+            pass
+    a = np.ascontiguousarray(np.asarray(xs, dtype=np.int32)).reshape(-1)
+    return (ctypes.c_int32 * a.size).from_buffer_copy(a), a.size
 
 
 class Pool:
@@ -165,6 +177,7 @@ class Pool:
         self.bf16_control = bf16_control
         self.Hkv, self.D = num_kv_heads, head_dim
         self.host_only = host_only
+        self.device_index = -1
         L = lib()
         sizes = [ctypes.c_size_t() for _ in range(4)]
         _check(L.mkv_pool_required_bytes(ctypes.byref(self.cfg), *[ctypes.byref(s) for s in sizes]),
@@ -180,6 +193,7 @@ class Pool:
             self.buffers = [torch.empty(max(b, 256), dtype=torch.uint8, device=dev)
                             for b in self.bytes]
             ptrs = [ctypes.c_void_p(b.data_ptr()) for b in self.buffers]
+            self.device_index = self.buffers[0].get_device()
         _check(L.mkv_pool_create(ctypes.byref(self.cfg), *ptrs, ctypes.byref(handle)),
                "mkv_pool_create")
         self.handle = handle
@@ -310,8 +324,9 @@ class Pool:
     def _stream(self, stream):
         """The given stream, or the current one of the pool's device."""
         import torch
-        s = stream if stream is not None else torch.cuda.current_stream(self.buffers[0].device)
-        return ctypes.c_void_p(s.cuda_stream)
+        if stream is not None:
+            return stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device_index)
 
     def rope(self, q, k, positions, inv_freq, axes=None, interleaved=False, q_out=None, k_out=None,
              stream=None):
@@ -323,29 +338,37 @@ class Pool:
         import torch
         if self.host_only:
             raise ValueError("host-only pools have no device")
-        dev = self.buffers[0].device
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be [rows, Hq, head_dim]")
-        rows, Hq = q.shape[0], q.shape[1]
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
-        k_out = torch.empty_like(k, memory_format=torch.contiguous_format) if k_out is None else k_out
-        (qp, qs), (kp, ks), (qo, qos), (ko, kos) = (
-            _rows_ptr(t, h, self.D, name, dev) for t, h, name in
-            ((q, Hq, "q"), (k, self.Hkv, "k"), (q_out, Hq, "q_out"), (k_out, self.Hkv, "k_out")))
-        pp, fp = _dev_ptr(positions, torch.int32, "positions"), _dev_ptr(inv_freq, torch.float32, "inv_freq")
-        pos_shape = tuple(positions.shape) if positions.dim() == 2 else (1,) + tuple(positions.shape)
-        if len(pos_shape) != 2 or pos_shape[1] != rows or inv_freq.dim() != 1:
-            raise ValueError(f"positions must be [{rows}] or [n_axes, {rows}], inv_freq [n_freq]")
-        if any(t.shape[0] != rows for t in (k, q_out, k_out)):
+        Hq, Hkv, D, dev = q.shape[1], self.Hkv, self.D, self.device_index
+        qp, qs, rows = _rows_ptr(q, Hq, D, "q", dev)
+        kp, ks, k_rows = _rows_ptr(k, Hkv, D, "k", dev)
+        if q_out is None:
+            q_out = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
+            qo, qos, q_rows = q_out.data_ptr(), Hq * D, rows
+        else:
+            qo, qos, q_rows = _rows_ptr(q_out, Hq, D, "q_out", dev)
+        if k_out is None:
+            k_out = torch.empty((rows, Hkv, D), dtype=k.dtype, device=k.device)
+            ko, kos, o_rows = k_out.data_ptr(), Hkv * D, rows
+        else:
+            ko, kos, o_rows = _rows_ptr(k_out, Hkv, D, "k_out", dev)
+        if k_rows != rows or q_rows != rows or o_rows != rows:
             raise ValueError(f"q, k and the outputs must all have {rows} rows")
-        if positions.device != dev or inv_freq.device != dev:
-            raise ValueError(f"positions and inv_freq must be on {dev}")
-        a, ap = (None, None) if axes is None else _i32_array(axes)
-        if a is not None and a.size != inv_freq.numel():
-            raise ValueError("axes must list an axis per frequency")
-        _check(lib().mkv_rope(self.handle, rows, pp, pos_shape[0], fp, inv_freq.numel(), ap,
-                              1 if interleaved else 0, qp, qs, qo, qos, Hq, kp, ks, ko, kos,
-                              self._stream(stream)), "mkv_rope")
+        pp, fp = _dev_ptr(positions, torch.int32, "positions"), _dev_ptr(inv_freq, torch.float32, "inv_freq")
+        n_axes = positions.shape[0] if positions.dim() == 2 else 1
+        if positions.dim() not in (1, 2) or positions.shape[-1] != rows or inv_freq.dim() != 1:
+            raise ValueError(f"positions must be [{rows}] or [n_axes, {rows}], inv_freq [n_freq]")
+        if positions.get_device() != dev or inv_freq.get_device() != dev:
+            raise ValueError(f"positions and inv_freq must be on cuda:{dev}")
+        n_freq = inv_freq.shape[0]
+        a = None
+        if axes is not None:
+            a, n = _i32_list(axes)
+            if n != n_freq:
+                raise ValueError("axes must list an axis per frequency")
+        _check(lib().mkv_rope(self.handle, rows, pp, n_axes, fp, n_freq, a, 1 if interleaved else 0,
+                              qp, qs, qo, qos, Hq, kp, ks, ko, kos, self._stream(stream)), "mkv_rope")
         return q_out, k_out
 
     def prompt_attention(self, q, k, v, n_tokens, sm_scale=None, out=None, stream=None):
@@ -354,24 +377,27 @@ class Pool:
         sum(n_tokens) are ignored, and in a given ``out`` left as they were
         (mkv_prompt_attention)."""
         import torch
-        n, np_ = _i32_array(n_tokens)
         if self.host_only:
             raise ValueError("host-only pools have no device")
-        dev = self.buffers[0].device
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be [rows, Hq, head_dim]")
-        Hq, rows = q.shape[1], int(n.astype(np.int64).clip(min=0).sum())
-        (qp, qs), (kp, ks), (vp, vs) = (_rows_ptr(t, h, self.D, name, dev) for t, h, name in
-                                        ((q, Hq, "q"), (k, self.Hkv, "k"), (v, self.Hkv, "v")))
-        if min(q.shape[0], k.shape[0], v.shape[0]) < rows:
+        n, count = _i32_list(n_tokens)
+        Hq, D, dev = q.shape[1], self.D, self.device_index
+        rows = sum(x for x in n if x > 0)  # (the library refuses a negative count)
+        qp, qs, q_rows = _rows_ptr(q, Hq, D, "q", dev)
+        kp, ks, k_rows = _rows_ptr(k, self.Hkv, D, "k", dev)
+        vp, vs, v_rows = _rows_ptr(v, self.Hkv, D, "v", dev)
+        if q_rows < rows or k_rows < rows or v_rows < rows:
             raise ValueError(f"q, k and v must have the {rows} rows of n_tokens")
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        op = _dev_ptr(out, torch.bfloat16, "out")
-        if out.device != dev or out.dim() != 3 or tuple(out.shape[1:]) != (Hq, self.D) or out.shape[0] < rows:
-            raise ValueError(f"out must be [{rows} or more, {Hq}, {self.D}] on {dev}")
-        scale = 1.0 / math.sqrt(self.D) if sm_scale is None else float(sm_scale)
-        _check(lib().mkv_prompt_attention(self.handle, np_, n.size, qp, qs, kp, ks, vp, vs, Hq, scale, op,
+            out = torch.empty((q_rows, Hq, D), dtype=q.dtype, device=q.device)
+            op = out.data_ptr()
+        else:
+            op, _, o_rows = _rows_ptr(out, Hq, D, "out", dev)
+            if o_rows < rows or not out.is_contiguous():
+                raise ValueError(f"out must be contiguous with the {rows} rows of n_tokens")
+        scale = D ** -0.5 if sm_scale is None else float(sm_scale)
+        _check(lib().mkv_prompt_attention(self.handle, n, count, qp, qs, kp, ks, vp, vs, Hq, scale, op,
                                           self._stream(stream)), "mkv_prompt_attention")
         return out
 
@@ -386,28 +412,28 @@ class Pool:
     def fork(self, src_ids, dst_ids, n_tokens=None, stream=None):
         """Give each empty sequence of ``dst_ids`` the first tokens (default: all) of its source,
         sharing full pages copy-on-write (mkv_seq_fork)."""
-        s, sp = _i32_array(src_ids)
-        d, dp = _i32_array(dst_ids)
-        n, np_ = (None, None) if n_tokens is None else _i32_array(n_tokens)
-        if d.size != s.size or (n is not None and n.size != s.size):
+        s, ns = _i32_list(src_ids)
+        d, nd = _i32_list(dst_ids)
+        n, nn = (None, ns) if n_tokens is None else _i32_list(n_tokens)
+        if nd != ns or nn != ns:
             raise ValueError("src_ids, dst_ids and n_tokens must have the same length")
         st = None if self.host_only else self._stream(stream)
-        _check(lib().mkv_seq_fork(self.handle, sp, dp, np_, s.size, st), "mkv_seq_fork")
+        _check(lib().mkv_seq_fork(self.handle, s, d, n, ns, st), "mkv_seq_fork")
 
     def truncate(self, seq_ids, n_tokens, stream=None):
         """Roll sequences back to their first ``n_tokens`` tokens (mkv_seq_truncate)."""
-        s, sp = _i32_array(seq_ids)
-        n, np_ = _i32_array(n_tokens)
-        if n.size != s.size:
+        s, ns = _i32_list(seq_ids)
+        n, nn = _i32_list(n_tokens)
+        if nn != ns:
             raise ValueError("seq_ids and n_tokens must have the same length")
         st = None if self.host_only else self._stream(stream)
-        _check(lib().mkv_seq_truncate(self.handle, sp, np_, s.size, st), "mkv_seq_truncate")
+        _check(lib().mkv_seq_truncate(self.handle, s, n, ns, st), "mkv_seq_truncate")
 
     def free(self, seq_ids, stream=None):
         """Free every page of several sequences (mkv_seq_free)."""
-        s, sp = _i32_array(seq_ids)
+        s, ns = _i32_list(seq_ids)
         st = None if self.host_only else self._stream(stream)
-        _check(lib().mkv_seq_free(self.handle, sp, s.size, st), "mkv_seq_free")
+        _check(lib().mkv_seq_free(self.handle, s, ns, st), "mkv_seq_free")
 
     def compact(self, stream=None):
         """Move pages so that the slots in use are the first ones of each slab's order; returns

@@ -108,7 +108,11 @@ struct RowMove {
   int32_t count;
 };
 constexpr int kPageMoveMax = 1200, kRowMoveMax = 960;
-struct PageOpParams {
+// (A launch's cost grows with its parameters: 30 KB take several microseconds, so that short lists go
+// in a smaller block.)
+constexpr int kPageMoveFew = 80, kRowMoveFew = 80;
+template <int PAGES, int ROWS>
+struct PageOpLists {
   uint8_t* fp8_slab;
   uint8_t* tq3_slab;
   int32_t* tables;
@@ -116,9 +120,10 @@ struct PageOpParams {
   int32_t D, max_seqs, max_pages;
   int32_t pieces;  // CTAs per page (set by the launcher)
   int32_t n_page, n_row;
-  PageMove page[kPageMoveMax];
-  RowMove row[kRowMoveMax];
+  PageMove page[PAGES];
+  RowMove row[ROWS];
 };
+using PageOpParams = PageOpLists<kPageMoveMax, kRowMoveMax>;
 
 // ------------------------------------------------------------------ materialise (debug / QC)
 // Dense fp32 copy of one sequence's dequantised K and V; never used by decode.
@@ -191,7 +196,7 @@ struct PromptSeq {
   int32_t len;       // tokens (> 0)
   int32_t unit_end;  // one past the prompt's last unit
 };
-constexpr int kPromptMaxSeqs = 2048;
+constexpr int kPromptMaxSeqs = 128;  // (1.5 KB of parameters: larger blocks cost launch time)
 constexpr int kPromptMaxGroup = 128;  // query heads per KV head: a tile holds them all
 struct PromptParams {
   uint16_t* out;      // bf16 bits [rows][Hq][D]

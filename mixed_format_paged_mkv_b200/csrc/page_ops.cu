@@ -3,7 +3,10 @@
 // (mkv_pool_compact).  All are one kernel over two lists: pages to copy or to cut, and runs of
 // block-table entries to copy or to unmap.
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
+
+#include <cstring>
 
 #include "device_util.cuh"
 #include "mkv_internal.h"
@@ -17,7 +20,8 @@ constexpr int kPieceBytes = kThreads * kVecs * 16;      // bytes of a page that 
 
 // CTAs [0, n_page * pieces): piece (blockIdx.x % pieces) of page move blockIdx.x / pieces; the
 // rest: one run of table entries each.
-__global__ void __launch_bounds__(kThreads) page_ops_kernel(const __grid_constant__ PageOpParams p) {
+template <class P>
+__global__ void __launch_bounds__(kThreads) page_ops_kernel(const __grid_constant__ P p) {
   const int pages = p.n_page * p.pieces;
   if (static_cast<int>(blockIdx.x) >= pages) {
     const RowMove r = p.row[blockIdx.x - pages];
@@ -79,7 +83,17 @@ cudaError_t launch_page_ops(PageOpParams& p, cudaStream_t s) {
   if (p.n_page + p.n_row <= 0) return cudaSuccess;
   const int64_t slot = p.fp8_slot_bytes > p.tq3_slot_bytes ? p.fp8_slot_bytes : p.tq3_slot_bytes;
   p.pieces = static_cast<int32_t>((slot + kPieceBytes - 1) / kPieceBytes);
-  page_ops_kernel<<<p.n_page * p.pieces + p.n_row, kThreads, 0, s>>>(p);
+  const unsigned grid = static_cast<unsigned>(p.n_page * p.pieces + p.n_row);
+  using Few = PageOpLists<kPageMoveFew, kRowMoveFew>;
+  if (p.n_page <= kPageMoveFew && p.n_row <= kRowMoveFew) {
+    Few f;
+    std::memcpy(&f, &p, offsetof(Few, page));
+    std::memcpy(f.page, p.page, p.n_page * sizeof(PageMove));
+    std::memcpy(f.row, p.row, p.n_row * sizeof(RowMove));
+    page_ops_kernel<<<grid, kThreads, 0, s>>>(f);
+  } else {
+    page_ops_kernel<<<grid, kThreads, 0, s>>>(p);
+  }
   return cudaGetLastError();
 }
 

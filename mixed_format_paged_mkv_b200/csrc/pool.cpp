@@ -49,48 +49,58 @@ int cuda_fail(cudaError_t e, const char* what) {
 }
 
 // Free slots handed out lowest rank first; rank = position in the slot order.  A slot that several
-// sequences share is free again when the last of them gives it back.
+// sequences share is free again when the last of them gives it back.  The free slots are a bit set
+// over the ranks with a word below which none is free, so taking and giving cost a few instructions
+// (a call may move tens of thousands of pages).
 struct Allocator {
   int32_t n = 0;
-  std::vector<int32_t> rank;
-  std::vector<int32_t> refs;   // sequences that hold the slot
-  std::vector<uint8_t> is_free;
-  std::vector<uint64_t> heap;  // (rank << 32) | slot, min-heap
+  std::vector<int32_t> rank;      // of each slot
+  std::vector<int32_t> slot_at;   // of each rank
+  std::vector<int32_t> refs;      // sequences that hold the slot (0: free)
+  std::vector<uint64_t> free_bits;  // bit r % 64 of word r / 64: the slot of rank r is free
+  size_t low = 0;                 // no word before this one has a free slot
   int32_t n_free = 0;
 
   void init(int32_t slots) {
     n = slots;
     rank.resize(n);
+    slot_at.resize(n);
     refs.assign(n, 0);
-    is_free.assign(n, 1);
-    for (int32_t i = 0; i < n; ++i) rank[i] = i;
+    for (int32_t i = 0; i < n; ++i) rank[i] = slot_at[i] = i;
+    rebuild();
+  }
+  void set_order(const int32_t* order) {
+    for (int32_t i = 0; i < n; ++i) {
+      rank[order[i]] = i;
+      slot_at[i] = order[i];
+    }
     rebuild();
   }
   void rebuild() {
-    heap.clear();
+    free_bits.assign((static_cast<size_t>(n) + 63) / 64, 0);
+    low = 0;
     n_free = 0;
     for (int32_t s = 0; s < n; ++s)
-      if (is_free[s]) {
-        heap.push_back((static_cast<uint64_t>(rank[s]) << 32) | static_cast<uint32_t>(s));
+      if (refs[s] == 0) {
+        free_bits[rank[s] >> 6] |= 1ull << (rank[s] & 63);
         ++n_free;
       }
-    std::make_heap(heap.begin(), heap.end(), std::greater<uint64_t>());
   }
-  int32_t take() {
-    std::pop_heap(heap.begin(), heap.end(), std::greater<uint64_t>());
-    const int32_t s = static_cast<int32_t>(heap.back() & 0xffffffffu);
-    heap.pop_back();
-    is_free[s] = 0;
+  bool free_rank(int32_t r) const { return free_bits[r >> 6] >> (r & 63) & 1; }
+  int32_t take() {  // (the callers have checked n_free)
+    while (free_bits[low] == 0) ++low;
+    const int32_t s = slot_at[low * 64 + static_cast<size_t>(__builtin_ctzll(free_bits[low]))];
+    free_bits[low] &= free_bits[low] - 1;
     refs[s] = 1;
     --n_free;
     return s;
   }
-  void give(int32_t s) {
-    if (--refs[s] > 0) return;
-    is_free[s] = 1;
+  void give(int32_t s, int32_t holders = 1) {
+    if ((refs[s] -= holders) > 0) return;
+    const size_t w = static_cast<size_t>(rank[s]) >> 6;
+    free_bits[w] |= 1ull << (rank[s] & 63);
+    low = std::min(low, w);
     ++n_free;
-    heap.push_back((static_cast<uint64_t>(rank[s]) << 32) | static_cast<uint32_t>(s));
-    std::push_heap(heap.begin(), heap.end(), std::greater<uint64_t>());
   }
 };
 
@@ -126,7 +136,7 @@ struct mkv_pool {
   int32_t* d_status = nullptr;
   int64_t fp8_slot_bytes = 0, tq3_slot_bytes = 0;
   int sm_count = 148;
-  int device = 0;  // device of the buffers (the current one at creation)
+  int device = 0;  // device of the buffers
   int decode_sms = 0;  // SMs decode plans for (0: all of the device's)
   std::vector<Seq> seqs;
   Allocator alloc[2];
@@ -691,6 +701,7 @@ int device_op(mkv_pool_t p, const char* what, F&& f) {
   }
   if (p->fail_after > 0) --p->fail_after;
   if (p->host_only) return MKV_OK;
+  const DeviceGuard guard(p->device);
   ++p->launches;
   const cudaError_t e = f();
   return e == cudaSuccess ? MKV_OK : cuda_fail(e, what);
@@ -701,7 +712,7 @@ struct PageOps {
   mkv_pool_t p;
   const char* what;
   void* stream;
-  std::unique_ptr<PageOpParams> prm{new PageOpParams};
+  std::unique_ptr<PageOpParams> prm{new PageOpParams};  // (its lists are not initialised)
   PageOps(mkv_pool_t pool, const char* name, void* st) : p(pool), what(name), stream(st) {
     prm->fp8_slab = p->fp8_slab;
     prm->tq3_slab = p->tq3_slab;
@@ -796,7 +807,8 @@ int mkv_pool_create(const mkv_pool_config* cfg, void* fp8_slab, void* tq3_slab,
   if (!host_only) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    p->device = dev;
+    cudaPointerAttributes at{};
+    p->device = cudaPointerGetAttributes(&at, fp8_slab) == cudaSuccess && at.type == cudaMemoryTypeDevice ? at.device : dev;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->sm_count, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
       e = cudaMemsetAsync(d_tables, 0xFF, static_cast<size_t>(cfg->max_seqs) * cfg->max_pages_per_seq * 4, 0);
@@ -831,8 +843,7 @@ int mkv_pool_set_slot_order(mkv_pool_t p, int32_t fmt, const int32_t* order, int
       return fail(MKV_ERR_INVALID_ARG, "order is not a permutation");
     seen[order[i]] = 1;
   }
-  for (int32_t i = 0; i < n; ++i) a.rank[order[i]] = i;
-  a.rebuild();
+  a.set_order(order);
   return ok();
 }
 
@@ -1639,7 +1650,7 @@ int mkv_seq_copy(mkv_pool_t p, int32_t src, int32_t dst, void* stream) {
 }
 
 int mkv_seq_fork(mkv_pool_t p, const int32_t* src_ids, const int32_t* dst_ids, const int32_t* n_tokens,
-                 int32_t n_forks, void* stream) {
+                 int32_t n_forks, void* stream) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (n_forks < 0 || (n_forks > 0 && (!src_ids || !dst_ids)))
     return fail(MKV_ERR_INVALID_ARG, "bad sequence list");
@@ -1684,7 +1695,19 @@ int mkv_seq_fork(mkv_pool_t p, const int32_t* src_ids, const int32_t* dst_ids, c
     for (auto it = taken.rbegin(); it != taken.rend(); ++it) p->alloc[0].give(*it);
     return rc;
   }
-  // ---- commit
+  // ---- commit: a shared page's count grows once by all branches of its source that reach it
+  std::vector<int32_t> by_src(n_forks);
+  for (int32_t i = 0; i < n_forks; ++i) by_src[i] = i;
+  std::sort(by_src.begin(), by_src.end(), [&](int32_t x, int32_t y) { return src_ids[x] < src_ids[y]; });
+  for (int32_t a = 0, b = 0; a < n_forks; a = b) {
+    const Seq& s = p->seqs[src_ids[by_src[a]]];
+    std::vector<int32_t> ends(s.table.size() + 1, 0);  // branches with that many full pages
+    int32_t reach = 0;
+    for (b = a; b < n_forks && src_ids[by_src[b]] == src_ids[by_src[a]]; ++b, ++reach)
+      ++ends[(n_tokens ? n_tokens[by_src[b]] : s.ctx) / kPageTokens];
+    for (size_t pg = 0; (reach -= ends[pg]) > 0; ++pg)
+      p->alloc[slab_of(fmt_of(s.table[pg]))].refs[slot_of(s.table[pg])] += reach;
+  }
   size_t next = 0;
   for (int32_t i = 0; i < n_forks; ++i) {
     const Seq& s = p->seqs[src_ids[i]];
@@ -1697,17 +1720,18 @@ int mkv_seq_fork(mkv_pool_t p, const int32_t* src_ids, const int32_t* dst_ids, c
     const auto end8 = std::lower_bound(s.fp8_pages.begin(), s.fp8_pages.end(), full);
     d.fp8_pages.assign(s.fp8_pages.begin(), end8);
     d.n3 = full - static_cast<int32_t>(d.fp8_pages.size());
-    for (int32_t e : d.table) ++p->alloc[slab_of(fmt_of(e))].refs[slot_of(e)];
     if (pages > full) {
       d.table.push_back(entry_of(p->page_fmt, taken[next++]));
       d.fp8_pages.push_back(full);
     }
   }
   return ok();
+} catch (const std::bad_alloc&) {
+  return fail(MKV_ERR_INVALID_ARG, "out of host memory");
 }
 
 int mkv_seq_truncate(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_tokens, int32_t n_seqs,
-                     void* stream) {
+                     void* stream) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (n_seqs < 0 || (n_seqs > 0 && (!seq_ids || !n_tokens)))
     return fail(MKV_ERR_INVALID_ARG, "bad sequence list");
@@ -1785,18 +1809,35 @@ int mkv_seq_truncate(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_toke
     if (cuts[next].new_slot != cuts[next].old_slot) p->alloc[0].give(cuts[next].new_slot);
   for (int32_t e : dropped) p->alloc[slab_of(fmt_of(e))].give(slot_of(e));
   return rc == MKV_OK ? ok() : rc;
+} catch (const std::bad_alloc&) {
+  return fail(MKV_ERR_INVALID_ARG, "out of host memory");
 }
 
-int mkv_seq_free(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, void* stream) {
+int mkv_seq_free(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, void* stream) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (n_seqs < 0 || (n_seqs > 0 && !seq_ids)) return fail(MKV_ERR_INVALID_ARG, "bad sequence list");
   if (int e = check_seq_list(p, seq_ids, n_seqs, nullptr)) return e;
   PageOps ops(p, "free launch", stream);
   auto commit = [&](int32_t a, int32_t b) {
-    for (int32_t i = a; i < b; ++i) {
-      Seq& s = p->seqs[seq_ids[i]];
-      for (int32_t e : s.table) p->alloc[slab_of(fmt_of(e))].give(slot_of(e));
-      s = Seq();
+    // neighbours in the list that share their first pages give those back together
+    for (int32_t i = a, k = a; i < b; i = k) {
+      const std::vector<int32_t>& t = p->seqs[seq_ids[i]].table;
+      size_t shared = t.size();
+      for (k = i + 1; k < b; ++k) {
+        const std::vector<int32_t>& u = p->seqs[seq_ids[k]].table;
+        const size_t most = std::min(shared, u.size());
+        const size_t same = std::mismatch(t.begin(), t.begin() + most, u.begin()).first - t.begin();
+        if (same < 16) break;
+        shared = same;
+      }
+      for (size_t pg = 0; pg < shared; ++pg)
+        p->alloc[slab_of(fmt_of(t[pg]))].give(slot_of(t[pg]), k - i);
+      for (int32_t q = i; q < k; ++q) {
+        Seq& s = p->seqs[seq_ids[q]];
+        for (size_t pg = shared; pg < s.table.size(); ++pg)
+          p->alloc[slab_of(fmt_of(s.table[pg]))].give(slot_of(s.table[pg]));
+      }
+      for (int32_t q = i; q < k; ++q) p->seqs[seq_ids[q]] = Seq();
     }
   };
   int rc = MKV_OK;
@@ -1814,9 +1855,11 @@ int mkv_seq_free(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, void* str
   if (rc != MKV_OK) return rc;
   commit(done, n_seqs);
   return ok();
+} catch (const std::bad_alloc&) {
+  return fail(MKV_ERR_INVALID_ARG, "out of host memory");
 }
 
-int mkv_pool_compact(mkv_pool_t p, int32_t* n_moved, void* stream) {
+int mkv_pool_compact(mkv_pool_t p, int32_t* n_moved, void* stream) try {
   if (n_moved) *n_moved = 0;
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   int rc = MKV_OK;
@@ -1824,15 +1867,12 @@ int mkv_pool_compact(mkv_pool_t p, int32_t* n_moved, void* stream) {
     Allocator& a = p->alloc[f];
     const int32_t held = a.n - a.n_free;
     // ---- stage: held slots past the first `held` of the order move to the free slots among them
-    std::vector<uint64_t> from, to;  // (rank << 32) | slot, in the end both by rank
-    for (int32_t s = 0; s < a.n; ++s)
-      if ((a.rank[s] >= held) != (a.is_free[s] != 0))
-        (a.is_free[s] ? to : from).push_back((static_cast<uint64_t>(a.rank[s]) << 32) | static_cast<uint32_t>(s));
+    std::vector<int32_t> from, to;
+    for (int32_t r = 0; r < a.n; ++r)
+      if ((r < held) == a.free_rank(r)) (r < held ? to : from).push_back(a.slot_at[r]);
     if (from.empty()) continue;
-    std::sort(from.begin(), from.end());
-    std::sort(to.begin(), to.end());
     std::vector<int32_t> index(a.n, -1);  // a moving slot's place in the list
-    for (size_t k = 0; k < from.size(); ++k) index[static_cast<uint32_t>(from[k])] = static_cast<int32_t>(k);
+    for (size_t k = 0; k < from.size(); ++k) index[from[k]] = static_cast<int32_t>(k);
     struct Owner { int32_t seq, page; };
     std::vector<Owner> owner(from.size());  // a sequence that holds it (the only one, or one of several)
     for (int32_t q = 0; q < p->cfg.max_seqs; ++q) {
@@ -1851,7 +1891,7 @@ int mkv_pool_compact(mkv_pool_t p, int32_t* n_moved, void* stream) {
         if ((rc = ops.flush()) != MKV_OK) break;
         done = k;
       }
-      const int32_t src = static_cast<int32_t>(from[k] & 0xffffffffu), dst = static_cast<int32_t>(to[k] & 0xffffffffu);
+      const int32_t src = from[k], dst = to[k];
       const uint8_t shared = a.refs[src] > 1 ? 1 : 0;
       ops.page({src, dst, shared ? owner[k].page : owner[k].seq * p->cfg.max_pages_per_seq + owner[k].page,
                 static_cast<uint8_t>(fmt), kPageTokens, shared, 0});
@@ -1863,19 +1903,18 @@ int mkv_pool_compact(mkv_pool_t p, int32_t* n_moved, void* stream) {
         if (slab_of(fmt_of(e)) != f) continue;
         const int32_t k = index[slot_of(e)];
         if (k >= 0 && static_cast<size_t>(k) < done)
-          e = entry_of(fmt, static_cast<int32_t>(to[k] & 0xffffffffu));
+          e = entry_of(fmt, to[k]);
       }
     for (size_t k = 0; k < done; ++k) {
-      const int32_t src = static_cast<int32_t>(from[k] & 0xffffffffu), dst = static_cast<int32_t>(to[k] & 0xffffffffu);
-      a.refs[dst] = a.refs[src];
-      a.refs[src] = 0;
-      a.is_free[dst] = 0;
-      a.is_free[src] = 1;
+      a.refs[to[k]] = a.refs[from[k]];
+      a.refs[from[k]] = 0;
     }
     a.rebuild();
     if (n_moved) *n_moved += static_cast<int32_t>(done);
   }
   return rc == MKV_OK ? ok() : rc;
+} catch (const std::bad_alloc&) {
+  return fail(MKV_ERR_INVALID_ARG, "out of host memory");
 }
 
 int mkv_get_block_table(mkv_pool_t p, int32_t seq, int32_t* host_out, int32_t cap,

@@ -30,6 +30,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "mkv_internal.h"
 #include "tc_util.cuh"
 
@@ -717,8 +719,15 @@ cudaError_t launch(const PromptParams& p, const CUtensorMap& q, const CUtensorMa
                    cudaStream_t s) {
   using C = Cfg<D>;
   auto* fn = &prompt_kernel<C>;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> prepared{0};  // devices whose limit is raised already, a bit a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   fn<<<static_cast<unsigned>(p.n_units * p.Hkv), C::THREADS, C::SMEM, s>>>(p, q, k, v);
   return cudaGetLastError();
 }

@@ -183,7 +183,7 @@ def test_many_prompts_span_launches():
     pool = pool_for(1, 64)
     n0 = pool.launch_count()
     out = pool.prompt_attention(q, k, v, lens)
-    assert pool.launch_count() - n0 == 2
+    assert pool.launch_count() - n0 == -(-2501 // 128)
     assert torch.equal(pool.prompt_attention(q[:6], k[:6], v[:6], (1, 2, 3)), out[:6])
     check(out[-5:], *reference(q[-5:], k[-5:], v[-5:], (5,), 64 ** -0.5))
 
