@@ -297,7 +297,7 @@ MKV_API int mkv_seq_free(mkv_pool_t pool, const int32_t* seq_ids, int32_t n_seqs
  * `held` slots of the slot order moves to a free slot among them (both in order), and the tables
  * follow.  Afterwards the slots in use are the first ones of the order (their counts: see
  * mkv_pool_stats), so a cache can be saved or moved as one range per slab.  *n_moved (may be NULL)
- * receives the pages moved.  A call split over several launches (more than 1200 pages of a
+ * receives the pages moved.  A call split over several launches (more than 850 runs of pages of a
  * format) takes effect launch by launch.  Errors: INVALID_ARG, CUDA. */
 MKV_API int mkv_pool_compact(mkv_pool_t pool, int32_t* n_moved, void* stream);
 
@@ -358,7 +358,7 @@ MKV_API int mkv_prefill_kv(mkv_pool_t pool, const int32_t* seq_ids, const int32_
  * An output overlaps no other array, but parts of one fused array may be rotated in place.  Any
  * stride of at least a row and 2-byte alignment work; 16-byte aligned rows with n_freq a multiple
  * of 8 are faster.  The angle is formed in 64 bits, so positions up to 2^31 keep their phase.
- * Errors: INVALID_ARG, CUDA. */
+ * Errors: INVALID_ARG, UNSUPPORTED (more than 65535 heads), CUDA. */
 MKV_API int mkv_rope(mkv_pool_t pool, int64_t rows, const int32_t* positions, int32_t n_axes,
                      const float* inv_freq, int32_t n_freq, const int32_t* axis_of, int32_t interleaved,
                      const void* q_in, int64_t q_in_stride, void* q_out, int64_t q_out_stride,

@@ -94,9 +94,12 @@ struct PackParams {
 };
 
 // ------------------------------------------------------------------ page operations
+// A run of pages: page i < count goes from slot src_slot + i to dst_slot + i, entry table_index + i.
+// (Sequences usually hold slots in order, so a few runs stand for thousands of pages.)
 struct PageMove {
   int32_t src_slot, dst_slot;  // equal: the page is cut where it is
   int32_t table_index;  // entry that gets the new slot; of a shared page its table column
+  int32_t first, count; // pages of the launch before this run, pages of the run
   uint8_t fmt;
   uint8_t kept;         // token rows kept; the others become zero (16: all kept)
   uint8_t shared;       // 1: every entry of the column that names the old slot gets the new one
@@ -107,7 +110,7 @@ struct RowMove {
   int32_t dst;    // first table index written
   int32_t count;
 };
-constexpr int kPageMoveMax = 1200, kRowMoveMax = 960;
+constexpr int kPageMoveMax = 850, kRowMoveMax = 960;
 // (A launch's cost grows with its parameters: 30 KB take several microseconds, so that short lists go
 // in a smaller block.)
 constexpr int kPageMoveFew = 80, kRowMoveFew = 80;
@@ -119,7 +122,8 @@ struct PageOpLists {
   int64_t fp8_slot_bytes, tq3_slot_bytes;
   int32_t D, max_seqs, max_pages;
   int32_t pieces;  // CTAs per page (set by the launcher)
-  int32_t n_page, n_row;
+  int32_t n_page, n_row;  // runs of pages, runs of table entries
+  int32_t pages;          // pages of all runs
   PageMove page[PAGES];
   RowMove row[ROWS];
 };
@@ -227,7 +231,8 @@ struct RopeParams {
   int32_t half;      // frequencies: the first 2 * half channels of a head are rotated
   int32_t next;      // 1: pairs of neighbouring channels, 0: of channels `half` apart
   int32_t vec;       // 1: 16-byte vectors (alignment and sizes checked on the host)
-  int32_t cta_rows;  // rows of a CTA (set by the launcher)
+  int32_t cta_rows;  // rows of a CTA, and 2^32 / (Hq + Hkv) rounded up (set by the launcher)
+  uint32_t heads_magic;
   uint8_t axis[128]; // axis of each frequency
 };
 

@@ -18,11 +18,11 @@ constexpr int kThreads = 256;
 constexpr int kVecs = 4;                                // 16-byte vectors a thread holds at once
 constexpr int kPieceBytes = kThreads * kVecs * 16;      // bytes of a page that one CTA copies
 
-// CTAs [0, n_page * pieces): piece (blockIdx.x % pieces) of page move blockIdx.x / pieces; the
-// rest: one run of table entries each.
+// CTAs [0, pages * pieces): piece (blockIdx.x % pieces) of page blockIdx.x / pieces; the rest: one
+// run of table entries each.
 template <class P>
 __global__ void __launch_bounds__(kThreads) page_ops_kernel(const __grid_constant__ P p) {
-  const int pages = p.n_page * p.pieces;
+  const int pages = p.pages * p.pieces;
   if (static_cast<int>(blockIdx.x) >= pages) {
     const RowMove r = p.row[blockIdx.x - pages];
     int32_t* dst = p.tables + r.dst;
@@ -34,8 +34,18 @@ __global__ void __launch_bounds__(kThreads) page_ops_kernel(const __grid_constan
     }
     return;
   }
-  const PageMove m = p.page[blockIdx.x / p.pieces];
-  const int piece = blockIdx.x % p.pieces;
+  const int page = blockIdx.x / p.pieces, piece = blockIdx.x % p.pieces;
+  int lo = 0, hi = p.n_page - 1;  // the run that holds the page
+  if (p.pages == p.n_page) lo = hi = page;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.page[mid].first <= page) lo = mid;
+    else hi = mid - 1;
+  }
+  PageMove m = p.page[lo];
+  m.src_slot += page - m.first;
+  m.dst_slot += page - m.first;
+  m.table_index += page - m.first;
   const bool tq3 = m.fmt == 1;
   const int64_t bytes = tq3 ? p.tq3_slot_bytes : p.fp8_slot_bytes;  // (BF16 pages: first slab)
   uint8_t* slab = tq3 ? p.tq3_slab : p.fp8_slab;
@@ -83,7 +93,7 @@ cudaError_t launch_page_ops(PageOpParams& p, cudaStream_t s) {
   if (p.n_page + p.n_row <= 0) return cudaSuccess;
   const int64_t slot = p.fp8_slot_bytes > p.tq3_slot_bytes ? p.fp8_slot_bytes : p.tq3_slot_bytes;
   p.pieces = static_cast<int32_t>((slot + kPieceBytes - 1) / kPieceBytes);
-  const unsigned grid = static_cast<unsigned>(p.n_page * p.pieces + p.n_row);
+  const unsigned grid = static_cast<unsigned>(p.pages * p.pieces + p.n_row);
   using Few = PageOpLists<kPageMoveFew, kRowMoveFew>;
   if (p.n_page <= kPageMoveFew && p.n_row <= kRowMoveFew) {
     Few f;

@@ -86,6 +86,12 @@ struct Allocator {
         ++n_free;
       }
   }
+  void set_free(int32_t s, bool f) {  // (the caller keeps n_free and refs right; low stays a bound)
+    const uint64_t bit = 1ull << (rank[s] & 63);
+    uint64_t& w = free_bits[static_cast<size_t>(rank[s]) >> 6];
+    w = f ? w | bit : w & ~bit;
+    if (f) low = std::min(low, static_cast<size_t>(rank[s]) >> 6);
+  }
   bool free_rank(int32_t r) const { return free_bits[r >> 6] >> (r & 63) & 1; }
   int32_t take() {  // (the callers have checked n_free)
     while (free_bits[low] == 0) ++low;
@@ -722,15 +728,26 @@ struct PageOps {
     prm->D = p->cfg.head_dim;
     prm->max_seqs = p->cfg.max_seqs;
     prm->max_pages = p->cfg.max_pages_per_seq;
-    prm->n_page = prm->n_row = 0;
+    prm->n_page = prm->n_row = prm->pages = 0;
   }
   bool fits(int pages, int rows) const {
     return prm->n_page + pages <= kPageMoveMax && prm->n_row + rows <= kRowMoveMax;
   }
-  int page(const PageMove& m) {
-    if (!fits(1, 0))
+  // The page of slot src goes to slot dst (the same slot: it is cut in place), entry or column index.
+  int page(int32_t src, int32_t dst, int32_t index, int fmt, int kept = kPageTokens, bool shared = false) {
+    if (prm->n_page > 0 && kept == kPageTokens && prm->pages < (1 << 26)) {
+      PageMove& l = prm->page[prm->n_page - 1];
+      if (l.kept == kPageTokens && l.fmt == fmt && l.shared == (shared ? 1 : 0) && src == l.src_slot + l.count &&
+          dst == l.dst_slot + l.count && index == l.table_index + l.count) {
+        ++l.count;
+        ++prm->pages;
+        return MKV_OK;
+      }
+    }
+    if (!fits(1, 0) || prm->pages >= (1 << 26))
       if (int e = flush()) return e;
-    prm->page[prm->n_page++] = m;
+    prm->page[prm->n_page++] = {src, dst, index, prm->pages++, 1, static_cast<uint8_t>(fmt),
+                                static_cast<uint8_t>(kept), static_cast<uint8_t>(shared ? 1 : 0), 0};
     return MKV_OK;
   }
   int row(const RowMove& m) {
@@ -742,7 +759,7 @@ struct PageOps {
   int flush() {
     if (prm->n_page + prm->n_row == 0) return MKV_OK;
     const int rc = device_op(p, what, [&] { return launch_page_ops(*prm, as_stream(stream)); });
-    prm->n_page = prm->n_row = 0;
+    prm->n_page = prm->n_row = prm->pages = 0;
     return rc;
   }
 };
@@ -1289,6 +1306,7 @@ int mkv_rope(mkv_pool_t p, int64_t rows, const int32_t* positions, int32_t n_axe
   const int Hkv = p->cfg.num_kv_heads, D = p->cfg.head_dim;
   if (rows < 0 || rows > INT32_MAX) return fail(MKV_ERR_INVALID_ARG, "rows out of range");
   if (Hq < Hkv || Hq % Hkv) return fail(MKV_ERR_INVALID_ARG, "num_q_heads %d not a multiple of Hkv %d", Hq, Hkv);
+  if (static_cast<int64_t>(Hq) + Hkv > 65535) return fail(MKV_ERR_UNSUPPORTED, "more than 65535 heads");
   if (n_axes < 1 || n_axes > 128) return fail(MKV_ERR_INVALID_ARG, "n_axes must be in [1, 128]");
   if (n_freq < 1 || 2 * static_cast<int64_t>(n_freq) > D)
     return fail(MKV_ERR_INVALID_ARG, "n_freq %d outside [1, head_dim / 2]", n_freq);
@@ -1636,9 +1654,8 @@ int mkv_seq_copy(mkv_pool_t p, int32_t src, int32_t dst, void* stream) {
   // ---- launch (the destination was empty: entries published before a failure are ignored)
   int rc = MKV_OK;
   for (size_t pg = 0; pg < s.table.size() && rc == MKV_OK; ++pg)
-    rc = ops.page({slot_of(s.table[pg]), slot_of(d.table[pg]),
-                   dst * p->cfg.max_pages_per_seq + static_cast<int32_t>(pg),
-                   static_cast<uint8_t>(fmt_of(s.table[pg])), kPageTokens, 0, 0});
+    rc = ops.page(slot_of(s.table[pg]), slot_of(d.table[pg]),
+                  dst * p->cfg.max_pages_per_seq + static_cast<int32_t>(pg), fmt_of(s.table[pg]));
   if (rc == MKV_OK) rc = ops.flush();
   if (rc != MKV_OK) {
     for (auto it = d.table.rbegin(); it != d.table.rend(); ++it)
@@ -1686,8 +1703,7 @@ int mkv_seq_fork(mkv_pool_t p, const int32_t* src_ids, const int32_t* dst_ids, c
     if (full > 0) rc = ops.row({src_ids[i] * MP, dst_ids[i] * MP, full});
     if (rc == MKV_OK && at % kPageTokens) {
       taken.push_back(p->alloc[0].take());
-      rc = ops.page({slot_of(s.table[full]), taken.back(), dst_ids[i] * MP + full,
-                     static_cast<uint8_t>(p->page_fmt), static_cast<uint8_t>(at % kPageTokens), 0, 0});
+      rc = ops.page(slot_of(s.table[full]), taken.back(), dst_ids[i] * MP + full, p->page_fmt, at % kPageTokens);
     }
   }
   if (rc == MKV_OK) rc = ops.flush();
@@ -1799,8 +1815,7 @@ int mkv_seq_truncate(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_toke
       const int32_t old_slot = slot_of(s.table[pg]);
       const int32_t slot = p->alloc[0].refs[old_slot] > 1 ? p->alloc[0].take() : old_slot;
       cuts.push_back({i, old_slot, slot});
-      ops.page({old_slot, slot, seq_ids[i] * MP + pg, static_cast<uint8_t>(p->page_fmt),
-                static_cast<uint8_t>(n_tokens[i] % kPageTokens), 0, 0});
+      ops.page(old_slot, slot, seq_ids[i] * MP + pg, p->page_fmt, n_tokens[i] % kPageTokens);
     }
   }
   if (rc == MKV_OK) rc = ops.flush();
@@ -1868,11 +1883,21 @@ int mkv_pool_compact(mkv_pool_t p, int32_t* n_moved, void* stream) try {
     const int32_t held = a.n - a.n_free;
     // ---- stage: held slots past the first `held` of the order move to the free slots among them
     std::vector<int32_t> from, to;
-    for (int32_t r = 0; r < a.n; ++r)
-      if ((r < held) == a.free_rank(r)) (r < held ? to : from).push_back(a.slot_at[r]);
+    for (int32_t r = held; r < a.n; ++r) {
+      if ((r & 63) == 0 && a.free_bits[r >> 6] == ~0ull) r += 63;  // 64 free slots
+      else if (!a.free_rank(r)) from.push_back(a.slot_at[r]);
+    }
     if (from.empty()) continue;
+    to.reserve(from.size());
+    for (size_t w = a.low; to.size() < from.size(); ++w)
+      for (uint64_t bits = a.free_bits[w]; bits && to.size() < from.size(); bits &= bits - 1)
+        to.push_back(a.slot_at[64 * w + static_cast<size_t>(__builtin_ctzll(bits))]);
     std::vector<int32_t> index(a.n, -1);  // a moving slot's place in the list
-    for (size_t k = 0; k < from.size(); ++k) index[from[k]] = static_cast<int32_t>(k);
+    bool any_shared = false;
+    for (size_t k = 0; k < from.size(); ++k) {
+      index[from[k]] = static_cast<int32_t>(k);
+      any_shared |= a.refs[from[k]] > 1;
+    }
     struct Owner { int32_t seq, page; };
     std::vector<Owner> owner(from.size());  // a sequence that holds it (the only one, or one of several)
     for (int32_t q = 0; q < p->cfg.max_seqs; ++q) {
@@ -1891,25 +1916,29 @@ int mkv_pool_compact(mkv_pool_t p, int32_t* n_moved, void* stream) try {
         if ((rc = ops.flush()) != MKV_OK) break;
         done = k;
       }
-      const int32_t src = from[k], dst = to[k];
-      const uint8_t shared = a.refs[src] > 1 ? 1 : 0;
-      ops.page({src, dst, shared ? owner[k].page : owner[k].seq * p->cfg.max_pages_per_seq + owner[k].page,
-                static_cast<uint8_t>(fmt), kPageTokens, shared, 0});
+      const bool shared = a.refs[from[k]] > 1;
+      ops.page(from[k], to[k],
+               shared ? owner[k].page : owner[k].seq * p->cfg.max_pages_per_seq + owner[k].page, fmt,
+               kPageTokens, shared);
     }
     if (rc == MKV_OK && (rc = ops.flush()) == MKV_OK) done = from.size();
     // ---- commit
-    for (Seq& s : p->seqs)
-      for (int32_t& e : s.table) {
-        if (slab_of(fmt_of(e)) != f) continue;
-        const int32_t k = index[slot_of(e)];
-        if (k >= 0 && static_cast<size_t>(k) < done)
-          e = entry_of(fmt, to[k]);
-      }
+    if (any_shared) {
+      for (Seq& s : p->seqs)
+        for (int32_t& e : s.table) {
+          if (slab_of(fmt_of(e)) != f) continue;
+          const int32_t k = index[slot_of(e)];
+          if (k >= 0 && static_cast<size_t>(k) < done) e = entry_of(fmt, to[k]);
+        }
+    } else {
+      for (size_t k = 0; k < done; ++k) p->seqs[owner[k].seq].table[owner[k].page] = entry_of(fmt, to[k]);
+    }
     for (size_t k = 0; k < done; ++k) {
       a.refs[to[k]] = a.refs[from[k]];
       a.refs[from[k]] = 0;
+      a.set_free(to[k], false);
+      a.set_free(from[k], true);
     }
-    a.rebuild();
     if (n_moved) *n_moved += static_cast<int32_t>(done);
   }
   return rc == MKV_OK ? ok() : rc;

@@ -14,6 +14,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "device_util.cuh"
 #include "mkv_internal.h"
 
@@ -49,54 +51,55 @@ __device__ __forceinline__ void rotate_word(uint32_t& w, float s, float c) {
 }
 
 // 16-byte vectors.  A unit is 16 channels: the vectors of 8 pairs (x[8u..], x[R/2 + 8u..]), two
-// neighbouring vectors with neighbouring pairs, or two neighbouring vectors that pass through.
-template <bool NEXT>
+// neighbouring vectors with neighbouring pairs, or two neighbouring vectors that pass through.  A CTA
+// takes as many rows as give each thread kUnits units, all of which it loads at once (128 bytes).
+constexpr int kUnits = 4;
+
+template <int D, bool NEXT>
 __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int U = 4;  // units a thread loads before the angles are needed
+  constexpr int kPer = D / 16;  // units of a head
   extern __shared__ __align__(16) float table[];
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.cta_rows;
   const int rows = static_cast<int>(min(static_cast<int64_t>(p.cta_rows), p.rows - row0));
   float* sn = table;
   float* cs = table + p.cta_rows * p.half;
-  const int heads = p.Hq + p.Hkv, per = p.D / 16, rot = p.half / 8;  // units a head, of which rotated
-  const int units = rows * heads * per;
+  const int heads = p.Hq + p.Hkv, rot = p.half / 8;  // (rot units of a head are rotated)
+  const int units = rows * heads * kPer;
   bool have_table = false;
-  for (int u0 = threadIdx.x; u0 < units || !have_table; u0 += U * kThreads) {
-    uint4 a[U], b[U];
-    uint4* oa[U];
-    int step[U];  // vectors from a unit's first to its second; 0: no unit
+  for (int u0 = threadIdx.x; u0 < units || !have_table; u0 += kUnits * kThreads) {
+    uint4 a[kUnits], b[kUnits];
+    uint4* to[kUnits];
+    int at[kUnits];  // first table entry of the unit's pairs, -1: passes through
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
+    for (int e = 0; e < kUnits; ++e) {
       const int u = u0 + e * kThreads;
-      step[e] = 0;
       if (u >= units) continue;
-      const int c = u % per, h = u / per % heads;
-      const int64_t r = row0 + u / per / heads;
+      const int c = u % kPer, i = u / kPer;
+      const int r = static_cast<int>(__umulhi(i, p.heads_magic)), h = i - r * heads;
       const bool is_q = h < p.Hq;
-      const int hh = is_q ? h : h - p.Hq;
-      const int first = NEXT || c >= rot ? 2 * c : c;
-      step[e] = NEXT || c >= rot ? 1 : p.half / 8;
-      const uint4* in = reinterpret_cast<const uint4*>(
-          (is_q ? p.q_in + r * p.q_in_stride : p.k_in + r * p.k_in_stride) + hh * p.D) + first;
-      oa[e] = reinterpret_cast<uint4*>(
-          (is_q ? p.q_out + r * p.q_out_stride : p.k_out + r * p.k_out_stride) + hh * p.D) + first;
-      a[e] = in[0];
-      b[e] = in[step[e]];
+      const uint16_t* in = is_q ? p.q_in + (row0 + r) * p.q_in_stride + h * D
+                                : p.k_in + (row0 + r) * p.k_in_stride + (h - p.Hq) * D;
+      uint16_t* out = is_q ? p.q_out + (row0 + r) * p.q_out_stride + h * D
+                           : p.k_out + (row0 + r) * p.k_out_stride + (h - p.Hq) * D;
+      const bool pair = NEXT || c >= rot;  // the unit's two vectors are neighbours
+      const int first = pair ? 2 * c : c, second = pair ? 2 * c + 1 : c + rot;
+      a[e] = reinterpret_cast<const uint4*>(in)[first];
+      b[e] = reinterpret_cast<const uint4*>(in)[second];
+      to[e] = reinterpret_cast<uint4*>(out) + first;
+      at[e] = c < rot ? r * p.half + 8 * c : -1;
     }
-    if (!have_table) {
+    if (!have_table) {  // (computed while the vectors are on their way)
       fill_table(p, row0, rows, sn, cs);
       __syncthreads();
       have_table = true;
     }
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
-      if (step[e] == 0) continue;
-      const int u = u0 + e * kThreads;
-      const int c = u % per, r = u / per / heads;
-      if (c < rot) {
+    for (int e = 0; e < kUnits; ++e) {
+      if (u0 + e * kThreads >= units) continue;
+      if (at[e] >= 0) {
         float s[8], k[8];
-        const float4* s4 = reinterpret_cast<const float4*>(sn + r * p.half + 8 * c);
-        const float4* c4 = reinterpret_cast<const float4*>(cs + r * p.half + 8 * c);
+        const float4* s4 = reinterpret_cast<const float4*>(sn + at[e]);
+        const float4* c4 = reinterpret_cast<const float4*>(cs + at[e]);
         *reinterpret_cast<float4*>(s) = s4[0];
         *reinterpret_cast<float4*>(s + 4) = s4[1];
         *reinterpret_cast<float4*>(k) = c4[0];
@@ -117,8 +120,8 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constan
           rotate(a[e].w, b[e].w, s + 6, k + 6);
         }
       }
-      oa[e][0] = a[e];
-      oa[e][step[e]] = b[e];
+      to[e][0] = a[e];
+      to[e][NEXT || at[e] < 0 ? 1 : rot] = b[e];
     }
   }
 }
@@ -152,12 +155,24 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
 
 cudaError_t launch_rope(RopeParams& p, cudaStream_t s) {
   if (p.rows <= 0) return cudaSuccess;
-  p.cta_rows = 1;
-  const unsigned grid = static_cast<unsigned>((p.rows + p.cta_rows - 1) / p.cta_rows);
-  const size_t smem = sizeof(float) * 2 * p.cta_rows * p.half;
+  const int64_t heads = p.Hq + p.Hkv, per_row = heads * (p.vec ? p.D / 16 : p.D / 2);
+  // rows of a CTA: kUnits units a thread, but no fewer CTAs than give every SM two (a decode step's few
+  // rows: measured 64 rows of 40 heads, D 128)
+  int64_t r = std::max<int64_t>(1, kUnits * kThreads / per_row);
+  r = std::min<int64_t>({r, 64, std::max<int64_t>(1, p.rows / 296)});
+  p.cta_rows = static_cast<int32_t>(r);
+  // i / heads for the units of a CTA (i < 2^32 / heads; at least two heads, one of q and one of k)
+  p.heads_magic = static_cast<uint32_t>((1ull << 32) / heads + 1);
+  const unsigned grid = static_cast<unsigned>((p.rows + r - 1) / r);
+  const size_t smem = sizeof(float) * 2 * r * p.half;
+#define MKV_ROPE(D)                                                   \
+  (p.next ? rope_vec_kernel<D, true><<<grid, kThreads, smem, s>>>(p)  \
+          : rope_vec_kernel<D, false><<<grid, kThreads, smem, s>>>(p))
   if (!p.vec) rope_any_kernel<<<grid, kThreads, smem, s>>>(p);
-  else if (p.next) rope_vec_kernel<true><<<grid, kThreads, smem, s>>>(p);
-  else rope_vec_kernel<false><<<grid, kThreads, smem, s>>>(p);
+  else if (p.D == 64) MKV_ROPE(64);
+  else if (p.D == 128) MKV_ROPE(128);
+  else MKV_ROPE(256);
+#undef MKV_ROPE
   return cudaGetLastError();
 }
 

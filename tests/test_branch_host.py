@@ -147,6 +147,7 @@ def test_demoting_one_holder_leaves_the_others_page():
 
 def small():
     p = Pool(1, 64, 3000, 40, 40000, 20000, host_only=True)
+    p.set_slot_order(0, np.random.default_rng(1).permutation(40000))   # (no runs of neighbouring slots)
     p.append([0, 1], [500, 77])
     p.demote([0], 48)
     return p
