@@ -210,6 +210,7 @@ struct PromptParams {
   float c;            // sm_scale * log2(e)
   int32_t Hkv, Hq, g, D;
   int32_t tile_tokens;  // tokens of a 128-row query tile
+  int32_t out32;        // 1: out is 32-byte aligned
   int32_t n_seqs, n_units;
   PromptSeq seq[kPromptMaxSeqs];  // longest first
 };

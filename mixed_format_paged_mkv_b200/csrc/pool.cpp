@@ -1424,6 +1424,7 @@ int mkv_prompt_attention(mkv_pool_t p, const int32_t* n_tokens, int32_t n_prompt
   prm->g = g;
   prm->D = D;
   prm->tile_tokens = 128 / g;
+  prm->out32 = (reinterpret_cast<uintptr_t>(out_bf16) & 31) == 0 ? 1 : 0;
   const PromptInputs inputs{q_bf16, k_bf16, v_bf16, q_stride, k_stride, v_stride, rows};
   const int64_t unit_tokens = static_cast<int64_t>(prm->tile_tokens) * prompt_tiles_per_unit(D);
   for (size_t b = 0; b < seqs.size();) {

@@ -194,13 +194,9 @@ __device__ __forceinline__ int64_t next_item(int n, B* b, int32_t* status) {
   return index;
 }
 
-// 8 bf16 values: whether one is infinite or NaN.
-__device__ __forceinline__ bool nonfinite8(const uint4& v) {
-  auto bad = [](uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-  };
-  return bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
-}
+// Two bf16 values: bits 15 and 31 say which are infinite or NaN (the sum carries into them from an
+// exponent of ones only); the other bits mean nothing.
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; }
 __device__ __forceinline__ uint32_t zero_nonfinite(uint32_t w) {
   if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
   if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
@@ -224,6 +220,19 @@ __device__ __forceinline__ void poly_exp2(uint64_t x, float& lo, float& hi) {
   q = mul2(q, f32x2(__uint_as_float(static_cast<uint32_t>(t) << 23), __uint_as_float(static_cast<uint32_t>(t >> 32) << 23)));
   lo = f32x2_lo(q);
   hi = f32x2_hi(q);
+}
+
+// 32 bytes to global memory, at once where the address allows: a row's lanes write to different rows,
+// and whole sectors halve the requests.
+__device__ __forceinline__ void store32(uint16_t* to, const uint32_t (&w)[8], int aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 template <class C>
@@ -504,20 +513,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!wait_bar_warp(&b->v_guard[s], (g_phase >> s) & 1, b, p.status)) return false;
         g_phase ^= 1u << s;
         if (!wait_bar_warp(&b->kv_full[s], ring.round & 1, b, p.status)) return false;
+        // (Half of what a guarded chunk costs is on the way to the prompt's output, so the scan is three
+        // instructions a word: with a test per value it took 5000 to 23000 cycles an item.)
         uint4* v = reinterpret_cast<uint4*>(skv + s * C::CHUNK);
-        bool found = false;
-#pragma unroll 4
-        for (int i = lane; i < C::CHUNK / 16; i += 32) {  // 16 bytes of one key's row
-          const int key = c0 + (i / 8) % VK;
+        uint32_t found = 0;
+#pragma unroll 8
+        for (int i = lane; i < C::CHUNK / 16; i += 32) {
           const uint4 x = v[i];
-          if (key >= it.len) {
-            v[i] = make_uint4(0, 0, 0, 0);
-          } else if (nonfinite8(x)) {
-            v[i] = make_uint4(zero_nonfinite(x.x), zero_nonfinite(x.y), zero_nonfinite(x.z), zero_nonfinite(x.w));
-            found = true;
+          found |= nonfinite_bits(x.x) | nonfinite_bits(x.y) | nonfinite_bits(x.z) | nonfinite_bits(x.w);
+        }
+        const bool past = c0 + VK > it.len;
+        const bool dirty = __any_sync(0xffffffffu, found & 0x80008000u);
+        if (past || dirty) {
+#pragma unroll 1
+          for (int i = lane; i < C::CHUNK / 16; i += 32) {  // 16 bytes of one key's row
+            const int key = c0 + (i / 8) % VK;
+            const uint4 x = v[i];
+            v[i] = key >= it.len ? make_uint4(0, 0, 0, 0)
+                                 : make_uint4(zero_nonfinite(x.x), zero_nonfinite(x.y), zero_nonfinite(x.z), zero_nonfinite(x.w));
           }
         }
-        if (found) *reinterpret_cast<volatile int32_t*>(&b->bad[n_item % kFlagSlots]) = n_item;
+        if (dirty && lane == 0) *reinterpret_cast<volatile int32_t*>(&b->bad[n_item % kFlagSlots]) = n_item;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // these stores -> tensor core
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->v_ready[s]);
@@ -640,26 +656,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const bool bad = *reinterpret_cast<volatile int32_t*>(&b->bad[n_item % kFlagSlots]) == n_item;
       uint16_t* out = p.out + (static_cast<int64_t>(it.row0 + pos) * p.Hq + it.h * p.g + gi) * D;
 #pragma unroll 1
-      for (int k = 0; k < D / 32; ++k) {
-        uint32_t x[32];
-        tmem_ld32(x, o_addr + 32 * k);
-        tmem_wait_ld(x);
+      for (int k = 0; k < D / 64; ++k) {  // 64 channels: 128 bytes of the row
+        uint32_t x[2][32];
+        tmem_ld32(x[0], o_addr + 64 * k);
+        tmem_ld32(x[1], o_addr + 64 * k + 32);
+        tmem_wait_ld(x[0]);
+        tmem_wait_ld(x[1]);
+        if (k + 1 == D / 64) {  // the tile's columns are free for the next item
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b->o_free[t]);
+        }
         if (mine) {
-          uint4* o4 = reinterpret_cast<uint4*>(out + 32 * k);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+            uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * e]) * inv, __uint_as_float(x[8 * i + 2 * e + 1]) * inv);
-            o4[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 8; ++e) {
+              const uint64_t o = mul2(f32x2(__uint_as_float(x[i / 2][16 * (i % 2) + 2 * e]),
+                                            __uint_as_float(x[i / 2][16 * (i % 2) + 2 * e + 1])),
+                                      f32x2(inv, inv));
+              w[e] = pack_bf16x2(f32x2_lo(o), f32x2_hi(o));
+            }
+            store32(out + 64 * k + 16 * i, w, p.out32);
           }
         }
         __syncwarp();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b->o_free[t]);
       if (mine && bad) {  // non-finite V elements that this row sees, of the chunks that the guard cleaned
 #pragma unroll 1
         for (int key = (it.t0 + 1) / VK * VK; key <= pos; ++key) {
