@@ -6,6 +6,7 @@ a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -154,16 +155,25 @@ def _rows_ptr(t, heads, dim, name, device):
     return t.data_ptr(), stride[0] if shape[0] > 1 else heads * dim, shape[0]
 
 
+def _empty_like(t, shape, stream):
+    """A new tensor of t's type and device, from the memory of the stream that will write it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=t.dtype, device=t.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=t.dtype, device=t.device)
+
+
 def _i32_list(xs):
-    """A host int32 array of a short list (cheaper than _i32_array's numpy for the list's sake) and
-    its length."""
+    """(address, length, owner) of a list's int32 values on the host; the owner keeps them alive."""
     if isinstance(xs, (list, tuple)):
         try:
-            return (ctypes.c_int32 * len(xs))(*xs), len(xs)
-        except TypeError:  # numpy integers and the like
+            a = array.array("i", xs)
+            return a.buffer_info()[0], len(a), a
+        except TypeError:  # elements that are no integers: numpy decides
             pass
     a = np.ascontiguousarray(np.asarray(xs, dtype=np.int32)).reshape(-1)
-    return (ctypes.c_int32 * a.size).from_buffer_copy(a), a.size
+    return a.ctypes.data, a.size, a
 
 
 class Pool:
@@ -344,12 +354,12 @@ class Pool:
         qp, qs, rows = _rows_ptr(q, Hq, D, "q", dev)
         kp, ks, k_rows = _rows_ptr(k, Hkv, D, "k", dev)
         if q_out is None:
-            q_out = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
+            q_out = _empty_like(q, (rows, Hq, D), stream)
             qo, qos, q_rows = q_out.data_ptr(), Hq * D, rows
         else:
             qo, qos, q_rows = _rows_ptr(q_out, Hq, D, "q_out", dev)
         if k_out is None:
-            k_out = torch.empty((rows, Hkv, D), dtype=k.dtype, device=k.device)
+            k_out = _empty_like(k, (rows, Hkv, D), stream)
             ko, kos, o_rows = k_out.data_ptr(), Hkv * D, rows
         else:
             ko, kos, o_rows = _rows_ptr(k_out, Hkv, D, "k_out", dev)
@@ -364,7 +374,7 @@ class Pool:
         n_freq = inv_freq.shape[0]
         a = None
         if axes is not None:
-            a, n = _i32_list(axes)
+            a, n, keep = _i32_list(axes)
             if n != n_freq:
                 raise ValueError("axes must list an axis per frequency")
         _check(lib().mkv_rope(self.handle, rows, pp, n_axes, fp, n_freq, a, 1 if interleaved else 0,
@@ -381,16 +391,16 @@ class Pool:
             raise ValueError("host-only pools have no device")
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be [rows, Hq, head_dim]")
-        n, count = _i32_list(n_tokens)
+        n, count, lens = _i32_list(n_tokens)
         Hq, D, dev = q.shape[1], self.D, self.device_index
-        rows = sum(x for x in n if x > 0)  # (the library refuses a negative count)
+        rows = int(sum(lens))  # (the library refuses a negative count)
         qp, qs, q_rows = _rows_ptr(q, Hq, D, "q", dev)
         kp, ks, k_rows = _rows_ptr(k, self.Hkv, D, "k", dev)
         vp, vs, v_rows = _rows_ptr(v, self.Hkv, D, "v", dev)
         if q_rows < rows or k_rows < rows or v_rows < rows:
             raise ValueError(f"q, k and v must have the {rows} rows of n_tokens")
         if out is None:
-            out = torch.empty((q_rows, Hq, D), dtype=q.dtype, device=q.device)
+            out = _empty_like(q, (q_rows, Hq, D), stream)
             op = out.data_ptr()
         else:
             op, _, o_rows = _rows_ptr(out, Hq, D, "out", dev)
@@ -406,15 +416,15 @@ class Pool:
         _check(lib().mkv_seq_reset(self.handle, seq, st), "mkv_seq_reset")
 
     def copy(self, src, dst, stream=None):
-        st = None if self.host_only else _stream_ptr(stream)
+        st = None if self.host_only else self._stream(stream)
         _check(lib().mkv_seq_copy(self.handle, src, dst, st), "mkv_seq_copy")
 
     def fork(self, src_ids, dst_ids, n_tokens=None, stream=None):
         """Give each empty sequence of ``dst_ids`` the first tokens (default: all) of its source,
         sharing full pages copy-on-write (mkv_seq_fork)."""
-        s, ns = _i32_list(src_ids)
-        d, nd = _i32_list(dst_ids)
-        n, nn = (None, ns) if n_tokens is None else _i32_list(n_tokens)
+        s, ns, _s = _i32_list(src_ids)
+        d, nd, _d = _i32_list(dst_ids)
+        n, nn, _n = (None, ns, None) if n_tokens is None else _i32_list(n_tokens)
         if nd != ns or nn != ns:
             raise ValueError("src_ids, dst_ids and n_tokens must have the same length")
         st = None if self.host_only else self._stream(stream)
@@ -422,8 +432,8 @@ class Pool:
 
     def truncate(self, seq_ids, n_tokens, stream=None):
         """Roll sequences back to their first ``n_tokens`` tokens (mkv_seq_truncate)."""
-        s, ns = _i32_list(seq_ids)
-        n, nn = _i32_list(n_tokens)
+        s, ns, _s = _i32_list(seq_ids)
+        n, nn, _n = _i32_list(n_tokens)
         if nn != ns:
             raise ValueError("seq_ids and n_tokens must have the same length")
         st = None if self.host_only else self._stream(stream)
@@ -431,7 +441,7 @@ class Pool:
 
     def free(self, seq_ids, stream=None):
         """Free every page of several sequences (mkv_seq_free)."""
-        s, ns = _i32_list(seq_ids)
+        s, ns, _s = _i32_list(seq_ids)
         st = None if self.host_only else self._stream(stream)
         _check(lib().mkv_seq_free(self.handle, s, ns, st), "mkv_seq_free")
 

@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be the same for the whole warp)
   const int TT = p.tile_tokens;
 
+  if (warp == C::GUARD && lane < 3) tensor_map_prefetch(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
   if (tid == 0) {
     mbar_init(&b->q_full, 1);
     mbar_init(&b->q_empty, NT);
@@ -288,82 +289,64 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   if (warp == C::PRODUCER) {
     // ---------------------------------------------------------------- producer
     if (lane == 0) {
-    Ring<ST> ring;  // the next chunk to load
-    int n_item = 0, asked = 0;
-    bool go = true;
-    // the item after next is asked for when every role has taken the one before it
-    auto ask = [&] {
-      const int s = asked & 1;
-      if (asked >= 2 && !wait_bar(&b->next_empty[s], ((asked >> 1) - 1) & 1, b, p.status)) return false;
-      {
+      Ring<ST> ring;  // the next chunk to load
+      int n_item = 0, asked = 0;
+      bool go = true;
+      // the item after next is asked for when every role has taken the one before it
+      auto ask = [&] {
+        const int s = asked & 1;
+        if (asked >= 2 && !wait_bar(&b->next_empty[s], ((asked >> 1) - 1) & 1, b, p.status)) return false;
         mbar_arrive_expect_tx(&b->next_full[s], 16);
         clc_request(&b->next[s], &b->next_full[s]);
-      }
-      ++asked;
-      return true;
-    };
-    ask();
-    for (;;) {
-      const int64_t idx = next_item<true>(n_item, b, p.status);
-      if (idx < 0) break;
-      if (n_item > 0 && !ask()) break;
-      const Item it = get_item(p, NT, idx);
-      int n = 0, tiles = 0;
+        ++asked;
+        return true;
+      };
+      // the stage of the ring's next chunk, once it is free
+      auto stage = [&] {
+        go = go && (ring.round == 0 || wait_bar(&b->kv_empty[ring.stage], (ring.round - 1) & 1, b, p.status));
+        if (go) mbar_arrive_expect_tx(&b->kv_full[ring.stage], C::CHUNK);
+        return ring.stage;
+      };
+      ask();
+      while (go) {
+        const int64_t idx = next_item<true>(n_item, b, p.status);
+        if (idx < 0) break;
+        if (n_item > 0 && !ask()) break;
+        const Item it = get_item(p, NT, idx);
+        int n = 0, tiles = 0;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int nt = key_steps<C>(it, t, TT);
-        n = max(n, nt);
-        tiles += nt > 0;
-      }
-      if (n_item > 0 && !wait_bar(&b->q_empty, (n_item - 1) & 1, b, p.status)) break;
-      ++n_item;
-      {
+        for (int t = 0; t < NT; ++t) {
+          const int nt = key_steps<C>(it, t, TT);
+          n = max(n, nt);
+          tiles += nt > 0;
+        }
+        if (n_item > 0 && !wait_bar(&b->q_empty, (n_item - 1) & 1, b, p.status)) break;
+        ++n_item;
         mbar_arrive_expect_tx(&b->q_full, tiles * BLK * TT * p.g * 128);
         for (int t = 0; t < tiles; ++t)
           for (int k = 0; k < BLK; ++k)
-            tma_load_4d(sq + t * C::Q_TILE + k * C::Q_BLOCK, &qmap, 64 * k, 0, it.h,
-                        it.row0 + it.t0 + t * TT, &b->q_full);
-      }
-      auto slot = [&] {  // waits until the ring's next chunk is free
-        return ring.round == 0 || wait_bar(&b->kv_empty[ring.stage], (ring.round - 1) & 1, b, p.status);
-      };
-      for (int j = -SB; go && j < n; ++j) {  // V of step j, then K of step j + SB
-        if (j >= 0) {
-#pragma unroll
-          for (int f = 0; f < VC; ++f) {
-            if (!(go = go && slot())) break;
-            {
-              uint64_t* bar = &b->kv_full[ring.stage];
-              mbar_arrive_expect_tx(bar, C::CHUNK);
-#pragma unroll
-              for (int k = 0; k < BLK; ++k)
-                tma_load_3d(skv + ring.stage * C::CHUNK + k * C::V_BLOCK, &vmap, 64 * k, it.h,
-                            it.row0 + KT * j + VK * f, bar);
-              if (guarded<C>(it, KT * j + VK * f)) mbar_arrive(&b->v_guard[ring.stage]);
-            }
+            tma_load_4d(sq + t * C::Q_TILE + k * C::Q_BLOCK, &qmap, 64 * k, 0, it.h, it.row0 + it.t0 + t * TT,
+                        &b->q_full);
+        for (int j = -SB; go && j < n; ++j) {  // V of step j, then K of step j + SB
+          for (int f = 0; go && f < VC && j >= 0; ++f) {
+            const int s = stage(), key = KT * j + VK * f;
+            if (!go) break;
+            for (int k = 0; k < BLK; ++k)
+              tma_load_3d(skv + s * C::CHUNK + k * C::V_BLOCK, &vmap, 64 * k, it.h, it.row0 + key, &b->kv_full[s]);
+            if (guarded<C>(it, key)) mbar_arrive(&b->v_guard[s]);
             ring.step();
           }
-        }
-        if (j + SB < n) {
-#pragma unroll
-          for (int f = 0; f < KC; ++f) {
-            if (!(go = go && slot())) break;
-            {
-              uint64_t* bar = &b->kv_full[ring.stage];
-              mbar_arrive_expect_tx(bar, C::CHUNK);
-#pragma unroll
-              for (int k = 0; k < C::KB; ++k)
-                tma_load_3d(skv + ring.stage * C::CHUNK + k * C::K_BLOCK, &kmap, 64 * (C::KB * f + k), it.h,
-                            it.row0 + KT * (j + SB), bar);
-            }
+          for (int f = 0; go && f < KC && j + SB < n; ++f) {
+            const int s = stage();
+            if (!go) break;
+            for (int k = 0; k < C::KB; ++k)
+              tma_load_3d(skv + s * C::CHUNK + k * C::K_BLOCK, &kmap, 64 * (C::KB * f + k), it.h,
+                          it.row0 + KT * (j + SB), &b->kv_full[s]);
             ring.step();
           }
         }
       }
-      if (!go) break;
-    }
-    // every copy and answer has landed and every chunk was consumed before the CTA ends
-    {
+      // every copy and answer has landed and every chunk was consumed before the CTA ends
       const uint64_t limit = *reinterpret_cast<volatile int32_t*>(&b->abort) ? 100000000ull : 2000000000ull;
       for (uint32_t s = 0; s < ST; ++s) {  // each stage's last round
         const uint32_t rounds = ring.round + (s < ring.stage ? 1 : 0);
@@ -373,7 +356,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
       if (n_item > 0) mbar_wait(&b->q_empty, (n_item - 1) & 1, limit);
       mbar_wait(&b->next_full[(asked - 1) & 1], ((asked - 1) >> 1) & 1, limit);
-    }
     }
     __syncwarp();
   } else if (warp >= C::MMA) {
@@ -400,7 +382,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int n = key_steps<C>(it, t, TT);
       const int nmax = NT == 1 ? n : max(n, key_steps<C>(it, 1 - t, TT));
       if (!(go = wait_spin(&b->q_full, n_item & 1, b, p.status))) break;
-      if (n > 0 && n_out++ > 0 && !(go = wait_spin(&b->o_free[t], n_out & 1, b, p.status))) break;
 #pragma unroll 1
       for (int j = -SB; go && j < nmax; ++j) {
         const int sb = j & 1, buf = t * SB + sb;
@@ -439,6 +420,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           ready = __all_sync(0xffffffffu, all);
         }
         if (pv) {
+          // (the last item's output has been read before the first product overwrites it)
+          if (j == 0 && n_out++ > 0 && !(go = wait_spin(&b->o_free[t], n_out & 1, b, p.status))) break;
 #pragma unroll
           for (int h = 0; h < PH; ++h) {  // 64 keys at a time, as the probabilities come
             constexpr int kPerChunk = C::VK / 64;

@@ -18,6 +18,9 @@ __device__ __forceinline__ bool elect_lane() {
 }
 
 // ------------------------------------------------------------------ tensor-map loads
+__device__ __forceinline__ void tensor_map_prefetch(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
                                             uint64_t* bar) {
   asm volatile(
