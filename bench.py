@@ -531,7 +531,8 @@ def run_reference(args, rank, world):
 # layer of the long-context workload), --mode canary (two 59,008-token sequences at the long
 # workload's head shape, mixed cache against an all-FP8 control: decode time and KV bytes per
 # token), --mode pack (bulk FP8 -> TQ3 demotion of an all-FP8 pool shaped like the batch-8
-# workload, in GB/s), --mode prefill (direct bf16 -> TQ3 packing of that workload's prompts) and
+# workload, in GB/s), --mode prefill (direct bf16 -> TQ3 packing of that workload's prompts), --mode
+# prompt (the prompt phase of a layer of it: rotary positions, prompt attention, prefill, branches) and
 # --mode materialise (dense fp32 K and V of that workload's sequences), --mode configs (decode
 # µs per call, algorithmic GB/s and roofline fractions of every workload configuration, L2
 # flushed before each call, and the steady-state append -> demote -> decode step).
@@ -763,6 +764,54 @@ def run_extra(args):
                           device_frac=round(dgbs / peak, 4), peak_source=peak_src,
                           note="one mkv_prefill_kv call (bf16 read, TQ3/FP8 pages written): ms is "
                                "the call span with host planning, device_ms the device work alone"))
+    elif args.mode == "prompt":
+        # one layer of the batch-8 workload's prompt phase: rotary positions, prompt attention, the
+        # prefill write, then four branches per prompt (device time of each call, L2 flushed before)
+        w = WORKLOADS[2]
+        pages, lens, seqs, per = w.pages(), w.lengths(), list(range(w.B)), 4
+        rows, n = sum(lens), sum(pages)
+        pool = Pool(w.Hkv, w.D, w.B * (per + 1), max(pages) + 2, n + 64, n + 64, device=device)
+        ks, vs = zip(*(w.kv(s, 0) for s in seqs))
+        k, v = _bf16_tensor(np.concatenate(ks), device), _bf16_tensor(np.concatenate(vs), device)
+        gen = torch.Generator(device=device).manual_seed(w.seed(0))
+        q = torch.randn((rows, w.Hq, w.D), generator=gen, device=device).to(torch.bfloat16)
+        pos = torch.cat([torch.arange(L, dtype=torch.int32) for L in lens]).to(device)
+        inv = torch.tensor([10000.0 ** (-2.0 * i / w.D) for i in range(w.D // 2)], device=device)
+        qr, kr, out = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q)
+        dst = [w.B + i for i in range(w.B * per)]
+        calls = {
+            "rope": lambda: pool.rope(q, k, pos, inv, q_out=qr, k_out=kr),
+            "attention": lambda: pool.prompt_attention(qr, kr, v, lens, out=out),
+            "prefill": lambda: pool.prefill(seqs, lens, kr, v, window=w.window),
+            "fork": lambda: pool.fork([i // per for i in range(w.B * per)], dst, [lens[i // per] - 1 for i in range(w.B * per)]),
+        }
+        stream = torch.cuda.current_stream()
+        times = {name: [] for name in calls}
+        for rep in range(8):
+            for name, call in calls.items():
+                _flush_l2(device)
+                torch.cuda._sleep(20_000_000)
+                e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                e0.record(stream)
+                call()
+                e1.record(stream)
+                torch.cuda.synchronize()
+                if rep >= 2:
+                    times[name].append(e0.elapsed_time(e1))
+            pool.free(dst + seqs)
+        pool.device_status()
+        heads = w.Hq + w.Hkv
+        flops = 2.0 * w.Hq * w.D * sum(L * (L + 1) for L in lens)
+        rope_bytes = 4 * rows * heads * w.D + 4 * rows
+        us = {name: statistics.median(t) * 1e3 for name, t in times.items()}
+        lines.append(dict(mode="prompt", workload=w.name, tokens=rows, rope_us=round(us["rope"], 1),
+                          rope_gbs=round(rope_bytes / us["rope"] / 1e3, 1),
+                          attention_us=round(us["attention"], 1),
+                          attention_tflops=round(flops / us["attention"] / 1e6, 1),
+                          prefill_us=round(us["prefill"], 1), fork_us=round(us["fork"], 1),
+                          branches=len(dst), peak_gbs=peak, peak_source=peak_src,
+                          note="device time per call, L2 flushed before each; attention_tflops "
+                               "counts the visible half of the scores"))
     elif args.mode == "materialise":
         w = WORKLOADS[2]
         pool = build_pool(w, 1, 3, device)
@@ -882,7 +931,7 @@ def main():
     ap.add_argument("--cpu-seconds", type=float, default=10.0)
     ap.add_argument("--fused", action="store_true", help="--mode profile: the fused kernel")
     ap.add_argument("--q-len", type=int, default=1, help="--mode profile: new tokens per sequence")
-    ap.add_argument("--mode", choices=["bench", "sweep", "canary", "pack", "prefill", "materialise",
+    ap.add_argument("--mode", choices=["bench", "sweep", "canary", "pack", "prefill", "prompt", "materialise",
                                        "configs", "ablation", "profile"],
                     default="bench",
                     help="extra studies on one GPU (one JSON line per point); default: the bench")
