@@ -116,6 +116,12 @@ struct Seq {
   std::vector<uint8_t> prot;      // protected flag per logical page
   int32_t ctx = 0;
   int32_t n3 = 0;
+  void clear() {  // (the lists keep their memory: branches come and go with every step)
+    table.clear();
+    fp8_pages.clear();
+    prot.clear();
+    ctx = n3 = 0;
+  }
 };
 
 inline int32_t entry_of(int fmt, int32_t slot) {
@@ -126,6 +132,16 @@ inline int fmt_of(int32_t e) { return static_cast<int>(static_cast<uint32_t>(e) 
 // control pool, use the first.
 inline int slab_of(int fmt) { return fmt == MKV_FMT_TQ3 ? 1 : 0; }
 inline int32_t slot_of(int32_t e) { return static_cast<int32_t>(static_cast<uint32_t>(e) & kSlotMask); }
+
+// Entries that two tables have in common at the front (compared in blocks: tables are long and
+// branches of one sequence differ in their last pages only).
+size_t common_prefix(const int32_t* a, const int32_t* b, size_t n) {
+  size_t i = 0;
+  for (size_t block = 1024; block >= 16; block /= 8)
+    while (i + block <= n && std::memcmp(a + i, b + i, block * sizeof(int32_t)) == 0) i += block;
+  while (i < n && a[i] == b[i]) ++i;
+  return i;
+}
 
 struct TimingRec {
   cudaEvent_t ev[3];  // before the partial kernel, between partial and merge, after the merge
@@ -1646,6 +1662,7 @@ int mkv_seq_copy(mkv_pool_t p, int32_t src, int32_t dst, void* stream) {
   d.prot = s.prot;
   d.n3 = s.n3;
   d.fp8_pages = s.fp8_pages;
+  d.table.reserve(s.table.size());
   PageOps ops(p, "copy launch", stream);
   for (size_t pg = 0; pg < s.table.size(); ++pg) {
     const int f = fmt_of(s.table[pg]);
@@ -1841,8 +1858,7 @@ int mkv_seq_free(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, void* str
       size_t shared = t.size();
       for (k = i + 1; k < b; ++k) {
         const std::vector<int32_t>& u = p->seqs[seq_ids[k]].table;
-        const size_t most = std::min(shared, u.size());
-        const size_t same = std::mismatch(t.begin(), t.begin() + most, u.begin()).first - t.begin();
+        const size_t same = common_prefix(t.data(), u.data(), std::min(shared, u.size()));
         if (same < 16) break;
         shared = same;
       }
@@ -1853,7 +1869,7 @@ int mkv_seq_free(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, void* str
         for (size_t pg = shared; pg < s.table.size(); ++pg)
           p->alloc[slab_of(fmt_of(s.table[pg]))].give(slot_of(s.table[pg]));
       }
-      for (int32_t q = i; q < k; ++q) p->seqs[seq_ids[q]] = Seq();
+      for (int32_t q = i; q < k; ++q) p->seqs[seq_ids[q]].clear();
     }
   };
   int rc = MKV_OK;
