@@ -159,9 +159,9 @@ def _empty_like(t, shape, stream):
     """A new tensor of t's type and device, from the memory of the stream that will write it."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=t.dtype, device=t.device)
+        return t.new_empty(shape)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=t.dtype, device=t.device)
+        return t.new_empty(shape)
 
 
 def _i32_list(xs):

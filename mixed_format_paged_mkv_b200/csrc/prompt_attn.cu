@@ -42,8 +42,10 @@ template <int D_>
 struct Cfg {
   static constexpr int D = D_;
   static constexpr int NT = D == 256 ? 1 : 2;     // query tiles of an item
-  static constexpr int SB = 2;                    // score buffers per tile
+  static constexpr int SB = D == 64 ? 3 : 2;      // score buffers per tile
   static constexpr int KT = D == 256 ? 128 : 64;  // keys of a step (of a score buffer)
+  static constexpr uint32_t OUT = NT * SB * KT;   // first output column in tensor memory
+  static_assert(OUT + NT * D <= 512, "tensor memory");
   static constexpr int PH = KT / 64;              // the probabilities of a step are handed on by 64 keys
   static constexpr int BLK = D / 64;              // 64-channel blocks (128 bytes: the swizzle span)
   // ring chunks: K of a step in KC chunks of all its keys and KB blocks each, V in VC chunks of VK
@@ -63,7 +65,6 @@ struct Cfg {
   static constexpr int WARPS = MMA + NT, THREADS = 32 * WARPS;
   static constexpr uint32_t IDESC_S = tc_idesc_bf16(128, KT, false);
   static constexpr uint32_t IDESC_PV = tc_idesc_bf16(128, D, true);
-  static constexpr int POLY = D == 64 ? 4 : 0;  // of 16 pairs of scores, those that poly_exp2 takes
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -71,7 +72,6 @@ struct Cfg {
 constexpr uint64_t kDescK = tc_smem_desc(0, 16, 1024);
 template <class C>
 constexpr uint64_t kDescV = tc_smem_desc(0, C::V_BLOCK, 1024);
-constexpr uint32_t kOutCol = 256;       // first output column in tensor memory
 constexpr float kRescaleAbove = 8.0f;   // log2 units a row's maximum may exceed its reference by
 constexpr int kFlagSlots = 8;           // items the guard may run ahead of the softmax warps
 
@@ -201,25 +201,6 @@ __device__ __forceinline__ uint32_t zero_nonfinite(uint32_t w) {
   if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
   if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
   return w;
-}
-
-// 2^x of two values, x <= 8, with the FMA pipe: x = n + r with n the nearest integer (the sum with
-// 1.5 2^23 + 127 rounds to it and leaves n + 127 in the low mantissa bits, from where a shift makes it
-// the exponent of 2^n), 2^r by a polynomial of degree 4 on [-1/2, 1/2] (minimax for the relative error
-// by the Remez exchange: 2.6e-6, 2^-18).  Below 2^-126.5 and for -inf the result is 0.  NaN gives 0: the
-// caller makes every score of such a row NaN, and those that go through ex2 keep it.
-__device__ __forceinline__ void poly_exp2(uint64_t x, float& lo, float& hi) {
-  const uint64_t y = f32x2(fmaxf(f32x2_lo(x), -127.f), fmaxf(f32x2_hi(x), -127.f));
-  const uint64_t t = add2(y, f32x2(12583039.f, 12583039.f));
-  const uint64_t n = add2(t, f32x2(-12583039.f, -12583039.f));
-  const uint64_t r = fma2(n, f32x2(-1.f, -1.f), y);
-  uint64_t q = fma2(r, f32x2(0.009570102207362652f, 0.009570102207362652f), f32x2(0.05591785907745361f, 0.05591785907745361f));
-  q = fma2(q, r, f32x2(0.240247443318367f, 0.240247443318367f));
-  q = fma2(q, r, f32x2(0.6931217908859253f, 0.6931217908859253f));
-  q = fma2(q, r, f32x2(0.9999992847442627f, 0.9999992847442627f));
-  q = mul2(q, f32x2(__uint_as_float(static_cast<uint32_t>(t) << 23), __uint_as_float(static_cast<uint32_t>(t >> 32) << 23)));
-  lo = f32x2_lo(q);
-  hi = f32x2_hi(q);
 }
 
 // 32 bytes to global memory, at once where the address allows: a row's lanes write to different rows,
@@ -373,7 +354,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t lead = elect_lane() ? 1u : 0u;
     // start addresses of the operands' descriptors, in units of 16 bytes
     const uint32_t q16 = (smem_addr(sq) + t * C::Q_TILE) >> 4, kv16 = smem_addr(skv) >> 4;
-    const uint32_t o = kOutCol + t * D;
+    const uint32_t o = C::OUT + t * D;
     bool go = true;
     for (int n_item = 0; go; ++n_item) {
       const int64_t idx = next_item<false>(n_item, b, p.status);
@@ -383,8 +364,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int nmax = NT == 1 ? n : max(n, key_steps<C>(it, 1 - t, TT));
       if (!(go = wait_spin(&b->q_full, n_item & 1, b, p.status))) break;
 #pragma unroll 1
-      for (int j = -SB; go && j < nmax; ++j) {
-        const int sb = j & 1, buf = t * SB + sb;
+      for (int j = -SB, sb = 0; go && j < nmax; ++j, sb = sb + 1 == SB ? 0 : sb + 1) {
+        const int buf = t * SB + sb;
         const bool do_v = j >= 0, do_k = j + SB < nmax;
         const bool pv = do_v && j < n, qk = do_k && j + SB < n;
         const Ring<ST> rv = ring, rk = do_v ? ring.plus(VC) : ring;  // V chunks of step j, K of j + SB
@@ -533,7 +514,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // ---------------------------------------------------------------- softmax and output
     const int t = warp / 4, r = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t o_addr = lane_base + kOutCol + t * D;
+    const uint32_t o_addr = lane_base + C::OUT + t * D;
     const int tok = min(r / p.g, TT - 1), gi = r - (r / p.g) * p.g;
     const float c = p.c;
     const uint64_t c2 = f32x2(c, c);
@@ -549,16 +530,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const bool mine = r < TT * p.g && pos < it.len;
       float m = -INFINITY;
       uint64_t l2 = 0;
-      // Waits for the product of step j.  (The scores of step j + 1 are there, so the product of step
-      // j - 1 is done: the parity of this buffer's barrier is at most a phase away.)
-      auto wait_product = [&](int j) {
-        const int sb = j & 1;
+      // Waits for the last product of buffer sb.  (A step's scores follow the product of SB steps
+      // before, so by the step after the one meant that buffer's barrier is at most a phase away.)
+      auto wait_product = [&](int sb) {
         const bool ok = wait_bar_warp(&b->o_done[t * SB + sb], (~phase >> sb) & 1, b, p.status);
         tc_fence_after();
         return ok;
       };
-      for (int j = 0; j < n; ++j) {
-        const int sb = j & 1, buf = t * SB + sb;
+      int last = 0;  // the last step's buffer
+      for (int j = 0, sb = 0; j < n; ++j, last = sb, sb = sb + 1 == SB ? 0 : sb + 1) {
+        const int buf = t * SB + sb;
         if (!(go = wait_bar_warp(&b->s_full[buf], (phase >> sb) & 1, b, p.status))) break;
         tc_fence_after();
         const uint32_t s_addr = lane_base + buf * KT;
@@ -576,11 +557,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < KT / 2; ++i)
-          mx[i % 4] = max3_nan(mx[i % 4], __uint_as_float(x[i / 16][2 * (i % 16)]),
+          mx[i % 4] = max3(mx[i % 4], __uint_as_float(x[i / 16][2 * (i % 16)]),
                                __uint_as_float(x[i / 16][2 * (i % 16) + 1]));
-        float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
-        // a visible score that is NaN or +inf makes the whole row NaN, as in the formula
-        if (!(top < INFINITY)) m = top = __uint_as_float(0x7fc00000u);
+        // (NaN is no maximum here; a visible score that is NaN or +inf makes its exponent, and with it
+        // the row's sum and output, NaN, as in the formula)
+        const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
         const bool up = (top - m) * c > kRescaleAbove;
         if (j == 0) {
           m = top;
@@ -589,7 +570,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const float a = up ? fast_exp2((m - mn) * c) : 1.f;
           m = mn;
           l2 = mul2(l2, f32x2(a, a));
-          if (!(go = wait_product(j - 1))) break;
+          if (!(go = wait_product(last))) break;
 #pragma unroll 1
           for (int k = 0; k < D / 16; ++k) {
             uint32_t o[16];
@@ -611,13 +592,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const uint32_t(&xs)[32] = x[2 * h + i / 16];
             const uint64_t z =
                 fma2(f32x2(__uint_as_float(xs[2 * (i % 16)]), __uint_as_float(xs[2 * (i % 16) + 1])), c2, mc2);
-            float p0, p1;
-            if (i % 16 < C::POLY) {
-              poly_exp2(z, p0, p1);
-            } else {
-              p0 = fast_exp2(f32x2_lo(z));
-              p1 = fast_exp2(f32x2_hi(z));
-            }
+            const float p0 = fast_exp2(f32x2_lo(z)), p1 = fast_exp2(f32x2_hi(z));
             uint64_t& l = i % 2 ? lb : la;
             l = add2(l, f32x2(p0, p1));
             pk[i] = pack_bf16x2(p0, p1);
@@ -633,7 +608,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
       if (!go) break;
       // ---- output
-      if (!(go = wait_product(n - 1))) break;
+      if (!(go = wait_product(last))) break;
       // (a row whose scores are all -inf has no weights: NaN, as in the formula)
       const float inv = m == -INFINITY ? __uint_as_float(0x7fc00000u) : 1.f / (f32x2_lo(l2) + f32x2_hi(l2));
       const bool bad = *reinterpret_cast<volatile int32_t*>(&b->bad[n_item % kFlagSlots]) == n_item;

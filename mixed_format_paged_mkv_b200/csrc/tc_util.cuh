@@ -170,10 +170,10 @@ __device__ __forceinline__ int64_t clc_answer(const void* answer) {
   return got ? static_cast<int64_t>(x) : -1;
 }
 
-// The largest of three; NaN if one of them is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+// The largest of three that is no NaN.
+__device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
