@@ -202,6 +202,7 @@ struct PromptSeq {
 };
 constexpr int kPromptMaxSeqs = 128;  // (1.5 KB of parameters: larger blocks cost launch time)
 constexpr int kPromptMaxGroup = 128;  // query heads per KV head: a tile holds them all
+constexpr float kPromptMaxScale = 65536.f;  // far beyond use; the softmax's exponents are fp32
 struct PromptParams {
   uint16_t* out;      // bf16 bits [rows][Hq][D]
   const uint16_t* v;  // for the values that cannot pass the tensor core (see prompt_attn.cu)

@@ -1393,8 +1393,8 @@ int mkv_prompt_attention(mkv_pool_t p, const int32_t* n_tokens, int32_t n_prompt
   const int Hkv = p->cfg.num_kv_heads, D = p->cfg.head_dim;
   if (Hq < Hkv || Hq % Hkv) return fail(MKV_ERR_INVALID_ARG, "num_q_heads %d not a multiple of Hkv %d", Hq, Hkv);
   const int g = Hq / Hkv;
-  if (!std::isfinite(sm_scale) || sm_scale < 0)
-    return fail(MKV_ERR_INVALID_ARG, "sm_scale must be finite and not negative");
+  if (!(sm_scale >= 0 && sm_scale <= kPromptMaxScale))
+    return fail(MKV_ERR_INVALID_ARG, "sm_scale must be in [0, %g]", static_cast<double>(kPromptMaxScale));
   if (g > kPromptMaxGroup)
     return fail(MKV_ERR_UNSUPPORTED, "num_q_heads / Hkv = %d > %d is not built", g, kPromptMaxGroup);
   int64_t rows = 0;

@@ -7,10 +7,12 @@
 //
 // Rows.  A tile holds 128 query rows of one KV head: floor(128 / g) tokens times the g heads that
 // share the KV head, token-major, so K and V are read once for all of them and only the keys up to
-// the tile's last token are visited.  A CTA works on items of NT tiles (D 64 and 128: two tiles,
-// whose softmax and tensor work alternate; D 256: one tile with two score buffers).
+// the tile's last token are visited.  An item is NT tiles of consecutive tokens (D 64 and 128: two,
+// which share K and V; D 256: one, whose output takes half of tensor memory).  A CTA (one per SM)
+// works on items until none is left; it gets the next one by cluster launch control, so items go to
+// whichever SM is free, the ones with most keys first.
 //
-// Roles (one CTA per SM):
+// Roles:
 //   softmax warps  4 per tile, one row per thread: scores from tensor memory, probabilities back
 //                  into it as bf16, running sum and reference in registers, output at the end
 //   producer       tensor-map loads of Q and of K/V chunks into a ring
@@ -20,13 +22,30 @@
 //                  the end and replaces non-finite V elements by zero, because 0 x inf would reach
 //                  rows that do not see them; the rows that do see them get them back at the end
 //
-// Tensor memory (512 columns): score buffers in columns 0-255 (128 fp32 columns each; the bf16
-// probabilities overwrite the scores they come from), outputs from column 256 on.
+// Tensor memory (512 columns): NT x SB score buffers of KT fp32 columns, whose first half the bf16
+// probabilities overwrite, then NT outputs of D columns.
 //
 // Precision: products of bf16 with fp32 sums; the softmax's maximum, sum and output are fp32.  The
-// probabilities are rounded to bf16 (relative 2^-9 each) because they are a tensor-core operand.
+// probabilities are rounded to bf16 (relative 2^-8 each) because they are a tensor-core operand.
 // The reference m moves only when a row's maximum exceeds it by more than 8 in log2 units, so
 // p <= 2^8 and the sums stay far inside fp32; each move rescales the fp32 output.
+//
+// Measured (one B200, one prompt of 8192 tokens, causal FLOPs): 32/8 heads, D 128: 440 us, 1250
+// TFLOP/s; 24/4 heads, D 256: 655 us, 1260 TFLOP/s; 16/16 heads, D 64: 199 us, 690 TFLOP/s.
+//   D 128: scores of 64 keys take 48 cycles per MMA instead of 32, since each reads 6 KB of operands
+//          from shared memory; with the products and the softmax's share of tensor memory the tensor
+//          path needs about 1600 of the 1740 cycles of a step.  Steps of 128 keys read less but leave
+//          room for one score buffer only, and then each tile's softmax and MMAs take turns: 493 us.
+//   D 256: one tile's chain: MMAs for 2050 of the 3250 cycles of a step, then what one step's scores,
+//          probabilities and products wait for one another; K and V come from L2 once per 128 rows
+//          (128 KB a step, 10 TB/s over all SMs, of 11.6 that loads alone reach), which adds 300.
+//   D 64:  the exponentials (16 a cycle and SM) are 1024 of the 1500 cycles of a step; two score
+//          buffers instead of three: 204 us.  Part of the exponentials as a polynomial on the FMA
+//          pipe: 218 us, the issue slots it takes cost more than the ex2 it saves.
+//   All:   one MMA warp for both tiles instead of one each: 614 us for 483 (D 128, at that step); the
+//          reference moved with every new maximum: 565 us for 438; (s - m) c in two operations instead
+//          of s c - m c in one: 490 us, so scores whose scaled size passes 2^30 (where the rounding of
+//          m c alone passes 2^6) may make their row NaN.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -567,7 +586,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           m = top;
         } else if (__any_sync(0xffffffffu, up)) {
           const float mn = up ? top : m;
-          const float a = up ? fast_exp2((m - mn) * c) : 1.f;
+          // (from the references as they are subtracted from scores, with their rounding)
+          const float a = up ? fast_exp2(__fsub_rn(__fmul_rn(m, c), __fmul_rn(mn, c))) : 1.f;
           m = mn;
           l2 = mul2(l2, f32x2(a, a));
           if (!(go = wait_product(last))) break;
@@ -581,7 +601,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             tmem_st16(o_addr + 16 * k, o);
           }
         }
-        const float mc = m == -INFINITY ? 0.f : m * c;
+        const float mc = m == -INFINITY ? 0.f : __fmul_rn(m, c);
         const uint64_t mc2 = f32x2(-mc, -mc);
         uint64_t la = 0, lb = 0;
 #pragma unroll

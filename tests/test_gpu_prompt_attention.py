@@ -229,3 +229,52 @@ def test_captured_and_overlapping_calls(D):
     for i, o in enumerate(outs):
         assert torch.equal(o, wa if i % 2 else wb), i
     pool.device_status()
+
+
+def test_more_than_2_to_the_31_elements():
+    """q and out hold 2.3e9 elements: the last prompts come out as in a call of their own."""
+    Hq, D, n = 128, 256, 700
+    lens = [100] * n + [33]
+    rows = sum(lens)
+    g = torch.Generator(device="cuda").manual_seed(21)
+    q = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device="cuda")
+    for a in range(0, rows, 10000):
+        q[a:a + 10000] = torch.randn(q[a:a + 10000].shape, generator=g, device="cuda")
+    k, v = (torch.randn((rows, 1, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    pool = pool_for(1, D)
+    out = pool.prompt_attention(q, k, v, np.array(lens))
+    assert out.numel() > 2 ** 31
+    tail = 3 * 100 + 33
+    assert torch.equal(out[-tail:], pool.prompt_attention(q[-tail:], k[-tail:], v[-tail:], (100, 100, 100, 33)))
+    assert torch.equal(out[:100], pool.prompt_attention(q[:100], k[:100], v[:100], (100,)))
+    check(out[-33:, :4], *reference(q[-33:, :4], k[-33:], v[-33:], (33,), D ** -0.5))
+    pool.device_status()
+
+
+def test_largest_and_smallest_scales():
+    """The limits of the softmax: the largest scale leaves each row its last key alone (its
+    probability and the result are rounded to bf16: 2 2^-8), a denormal one weighs all alike."""
+    q, k, v = make((40,), 1, 1, 64, seed=22)
+    q = q.abs() + 0.5
+    k[:, 0] = torch.arange(1, 41, device="cuda")[:, None].to(torch.bfloat16)   # the last key wins
+    pool = pool_for(1, 64)
+    out = pool.prompt_attention(q, k, v, (40,), sm_scale=65536.0).double()
+    assert bool(((out - v.double()).abs() <= 2.0 ** -7 * v.double().abs()).all())
+    check(pool.prompt_attention(q, k, v, (40,), sm_scale=1e-44), *reference(q, k, v, (40,), 0.0))
+    pool.device_status()
+
+
+def test_large_scores_keep_the_weights_of_moved_references():
+    """Scaled scores near 3000 whose maximum rises with every key tile: the rounding of a reference is
+    2^-24 of it and must not come between tiles."""
+    n, D = 512, 128
+    q = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    k, v = torch.zeros_like(q), make((n,), 1, 1, D, seed=23)[2]
+    q[:, 0, 0], q[:, 0, 1] = 1.0, 1.0
+    k[:, 0, 0] = 3008.0                                              # the same for all keys
+    k[:, 0, 1] = (torch.arange(n, device="cuda") // 64 * 8).to(torch.bfloat16)   # + 8 (11.5 in log2) a tile
+    pool = pool_for(1, D)
+    check(pool.prompt_attention(q, k, v, (n,), sm_scale=1.0), *reference(q, k, v, (n,), 1.0))
+    k[:, 0, 1] = (torch.arange(n, device="cuda") // 64 * 6).to(torch.bfloat16)   # + 6 (8.7): weights 1/403
+    check(pool.prompt_attention(q, k, v, (n,), sm_scale=1.0), *reference(q, k, v, (n,), 1.0))
+    pool.device_status()

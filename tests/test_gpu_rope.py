@@ -125,3 +125,20 @@ def test_no_rows_captured_and_other_streams():
     torch.cuda.synchronize()
     assert torch.equal(out[0], wb[0]) and torch.equal(out[1], wb[1])
     assert torch.equal(other[0], wa[0]) and torch.equal(other[1], wa[1])
+
+
+def test_more_than_2_to_the_31_elements():
+    """q holds 2.3e9 elements: the first and the last rows come out as in calls of their own."""
+    Hq, D, rows = 128, 256, 70001
+    pool = Pool(1, D, 1, 1, 1, 1)
+    _, _, pos, inv = make(rows, 1, 1, D, 1, D, seed=9)
+    q = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device="cuda")
+    for a in range(0, rows, 10000):
+        q[a:a + 10000] = torch.randn(q[a:a + 10000].shape, device="cuda")
+    k = torch.randn((rows, 1, D), device="cuda").to(torch.bfloat16)
+    qo, ko = pool.rope(q, k, pos, inv)
+    assert qo.numel() > 2 ** 31
+    for part in (slice(0, 5), slice(rows - 5, rows)):
+        a, b = pool.rope(q[part], k[part], pos[:, part].contiguous(), inv)
+        assert torch.equal(a, qo[part]) and torch.equal(b, ko[part])
+        check(qo[part], q[part], pos[:, part], inv, None, False)

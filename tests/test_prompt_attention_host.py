@@ -42,6 +42,9 @@ def test_null_pool():
     (dict(scale=float("nan")), INVALID_ARG, "sm_scale"),
     (dict(scale=float("inf")), INVALID_ARG, "sm_scale"),
     (dict(scale=-0.5), INVALID_ARG, "sm_scale"),
+    (dict(scale=65537.0), INVALID_ARG, "sm_scale"),
+    (dict(scale=1e30), INVALID_ARG, "sm_scale"),
+    (dict(scale=65536.0), INVALID_ARG, "host-only"),
     (dict(lens=(1 << 30, 1 << 30)), INVALID_ARG, "too many"),
     (dict(q=0), INVALID_ARG, "NULL"),
     (dict(k=0), INVALID_ARG, "NULL"),
