@@ -379,9 +379,9 @@ MKV_API int mkv_rope(mkv_pool_t pool, int64_t rows, const int32_t* positions, in
  * no input.  A masked key or value never reaches an output, also where it is infinite or NaN;
  * visible ones propagate as in the formula.  Sums and the softmax are fp32; the probabilities are
  * rounded to bf16 before they multiply v, the result once more; values of v beyond 2^96 may overflow
- * the fp32 sums, scores that sm_scale makes larger than 2^30 their row's softmax.  Needs no workspace and keeps no state: calls may overlap on different streams and
- * may be captured.  Errors: INVALID_ARG (also
- * sm_scale outside [0, 65536]), UNSUPPORTED (g > 128), CUDA. */
+ * the fp32 sums, scores that sm_scale makes larger than 2^30 their row's softmax.  Needs no
+ * workspace and keeps no state: calls may overlap on different streams and may be captured.
+ * Errors: INVALID_ARG (also sm_scale outside [0, 65536]), UNSUPPORTED (g > 128), CUDA. */
 MKV_API int mkv_prompt_attention(mkv_pool_t pool, const int32_t* n_tokens, int32_t n_prompts,
                                  const void* q_bf16, int64_t q_stride, const void* k_bf16,
                                  int64_t k_stride, const void* v_bf16, int64_t v_stride,
