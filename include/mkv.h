@@ -39,9 +39,10 @@
  *
  * Ownership: every device buffer is allocated and owned by the caller (e.g. by PyTorch) and
  * must outlive the pool; the pool owns only host state (allocators, the host copy of the
- * tables, protection flags).  All device work is asynchronous on the caller's stream
- * (a cudaStream_t passed as void*; NULL = legacy default stream); inputs must stay valid until
- * the stream reaches the call.  Calls on one pool must come from one host thread at a time and
+ * tables, protection flags).  Every call works on the device of the pool's buffers, whichever is
+ * current, and leaves the current one as it was.  All device work is asynchronous on the caller's
+ * stream (a cudaStream_t of that device passed as void*; NULL = its legacy default stream); inputs
+ * and outputs lie on that device and must stay valid until the stream reaches the call.  Calls on one pool must come from one host thread at a time and
  * be ordered on one stream (or ordered by the caller): slots freed by a call are reused by
  * later calls in stream order.
  *
@@ -124,8 +125,8 @@ MKV_API int mkv_pool_required_bytes(const mkv_pool_config* cfg, size_t* fp8_slab
                                     size_t* status_bytes);
 
 /* Create a pool over caller-owned device buffers (sizes from mkv_pool_required_bytes; each
- * 256-byte aligned).  The table is set to "unmapped" and the status word cleared on the
- * legacy default stream, which is synchronised before return.  With MKV_POOL_HOST_ONLY all
+ * 256-byte aligned, all on one device).  The table is set to "unmapped" and the status word cleared
+ * on its legacy default stream, which is synchronised before return.  With MKV_POOL_HOST_ONLY all
  * four pointers must be NULL and only host state is kept.  *out receives the handle. */
 MKV_API int mkv_pool_create(const mkv_pool_config* cfg, void* fp8_slab, void* tq3_slab,
                             int32_t* d_tables, int32_t* d_status, mkv_pool_t* out);

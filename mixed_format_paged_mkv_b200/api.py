@@ -120,13 +120,7 @@ def _i32_array(xs):
     return a, a.ctypes.data_as(_I32P)
 
 
-def _stream_ptr(stream=None):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
-
-
-def _dev_ptr(t, dtype, name):
+def _dev_ptr(t, dtype, name, device):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -134,6 +128,8 @@ def _dev_ptr(t, dtype, name):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    if device >= 0 and t.get_device() != device:  # (a host-only pool has none)
+        raise ValueError(f"{name} is on {t.device}, the pool on cuda:{device}")
     return ctypes.c_void_p(t.data_ptr())
 
 
@@ -233,12 +229,12 @@ class Pool:
             kp = vp = None
             st = None
         else:
-            kp = _dev_ptr(k, torch.bfloat16, "k")
-            vp = _dev_ptr(v, torch.bfloat16, "v")
+            kp = _dev_ptr(k, torch.bfloat16, "k", self.device_index)
+            vp = _dev_ptr(v, torch.bfloat16, "v", self.device_index)
             rows = int(n.sum())
             if tuple(k.shape) != (rows, self.Hkv, self.D) or tuple(v.shape) != (rows, self.Hkv, self.D):
                 raise ValueError(f"k, v must be [{rows}, {self.Hkv}, {self.D}]")
-            st = _stream_ptr(stream)
+            st = self._stream(stream)
         _check(lib().mkv_append_kv(self.handle, sp, np_, s.size, kp, vp, st), "mkv_append_kv")
 
     def prefill(self, seq_ids, n_tokens, k=None, v=None, window=0, stream=None):
@@ -251,18 +247,18 @@ class Pool:
             kp = vp = None
             st = None
         else:
-            kp = _dev_ptr(k, torch.bfloat16, "k")
-            vp = _dev_ptr(v, torch.bfloat16, "v")
+            kp = _dev_ptr(k, torch.bfloat16, "k", self.device_index)
+            vp = _dev_ptr(v, torch.bfloat16, "v", self.device_index)
             rows = int(n.sum())
             if tuple(k.shape) != (rows, self.Hkv, self.D) or tuple(v.shape) != (rows, self.Hkv, self.D):
                 raise ValueError(f"k, v must be [{rows}, {self.Hkv}, {self.D}]")
-            st = _stream_ptr(stream)
+            st = self._stream(stream)
         _check(lib().mkv_prefill_kv(self.handle, sp, np_, s.size, kp, vp, int(window), st),
                "mkv_prefill_kv")
 
     def selftest_wait(self, limit_ns=1_000_000, stream=None):
         """Launch the bounded-wait self-test; the next device_status() raises DEVICE_TIMEOUT."""
-        st = None if self.host_only else _stream_ptr(stream)
+        st = self._stream(stream)
         _check(lib().mkv_selftest_wait(self.handle, int(limit_ns), st), "mkv_selftest_wait")
 
     def selftest_tc_logits(self, a, q, stream=None):
@@ -272,9 +268,10 @@ class Pool:
         if tuple(a.shape) != (128, 256) or tuple(q.shape) != (8, 256):
             raise ValueError("a must be [128, 256] and q [8, 256]")
         d = torch.empty((128, 8), dtype=torch.float32, device=a.device)
-        _check(lib().mkv_selftest_tc_logits(self.handle, _dev_ptr(a, torch.float16, "a"),
-                                            _dev_ptr(q, torch.float16, "q"),
-                                            _dev_ptr(d, torch.float32, "d"), _stream_ptr(stream)),
+        dev = self.device_index
+        _check(lib().mkv_selftest_tc_logits(self.handle, _dev_ptr(a, torch.float16, "a", dev),
+                                            _dev_ptr(q, torch.float16, "q", dev),
+                                            _dev_ptr(d, torch.float32, "d", dev), self._stream(stream)),
                "mkv_selftest_tc_logits")
         return d
 
@@ -284,7 +281,7 @@ class Pool:
     def demote(self, seq_ids, window_tokens, stream=None):
         s, sp = _i32_array(seq_ids)
         n = ctypes.c_int32(0)
-        st = None if self.host_only else _stream_ptr(stream)
+        st = self._stream(stream)
         _check(lib().mkv_demote_pages(self.handle, sp, s.size, window_tokens, ctypes.byref(n), st),
                "mkv_demote_pages")
         return n.value
@@ -317,23 +314,25 @@ class Pool:
         n, q_len, Hq, D = q.shape
         if n != s.size or D != self.D:
             raise ValueError("q must be [len(seq_ids), q_len, Hq, head_dim]")
-        qp = _dev_ptr(q, torch.bfloat16, "q")
+        qp = _dev_ptr(q, torch.bfloat16, "q", self.device_index)
         if out is None:
             out = torch.empty((n, q_len, Hq, D), dtype=torch.float32, device=q.device)
-        op = _dev_ptr(out, torch.float32, "out")
+        op = _dev_ptr(out, torch.float32, "out", self.device_index)
         if workspace is None:   # the library checks a caller-given workspace's size itself
             workspace = torch.empty(self.workspace_bytes(s, q_len, Hq), dtype=torch.uint8,
                                     device=q.device)
-        wp = _dev_ptr(workspace, torch.uint8, "workspace")
+        wp = _dev_ptr(workspace, torch.uint8, "workspace", self.device_index)
         scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
         _check(lib().mkv_decode_attention(self.handle, sp, s.size, q_len, qp, Hq,
                                           ctypes.c_float(scale), op, wp, workspace.numel(),
-                                          _stream_ptr(stream)), "mkv_decode_attention")
+                                          self._stream(stream)), "mkv_decode_attention")
         return out
 
     def _stream(self, stream):
-        """The given stream, or the current one of the pool's device."""
+        """The given stream (of the pool's device), or the current one of the pool's device."""
         import torch
+        if self.host_only:
+            return None
         if stream is not None:
             return stream.cuda_stream
         return torch._C._cuda_getCurrentRawStream(self.device_index)
@@ -365,12 +364,11 @@ class Pool:
             ko, kos, o_rows = _rows_ptr(k_out, Hkv, D, "k_out", dev)
         if k_rows != rows or q_rows != rows or o_rows != rows:
             raise ValueError(f"q, k and the outputs must all have {rows} rows")
-        pp, fp = _dev_ptr(positions, torch.int32, "positions"), _dev_ptr(inv_freq, torch.float32, "inv_freq")
+        pp = _dev_ptr(positions, torch.int32, "positions", dev)
+        fp = _dev_ptr(inv_freq, torch.float32, "inv_freq", dev)
         n_axes = positions.shape[0] if positions.dim() == 2 else 1
         if positions.dim() not in (1, 2) or positions.shape[-1] != rows or inv_freq.dim() != 1:
             raise ValueError(f"positions must be [{rows}] or [n_axes, {rows}], inv_freq [n_freq]")
-        if positions.get_device() != dev or inv_freq.get_device() != dev:
-            raise ValueError(f"positions and inv_freq must be on cuda:{dev}")
         n_freq = inv_freq.shape[0]
         a = None
         if axes is not None:
@@ -412,11 +410,11 @@ class Pool:
         return out
 
     def reset(self, seq, stream=None):
-        st = None if self.host_only else _stream_ptr(stream)
+        st = self._stream(stream)
         _check(lib().mkv_seq_reset(self.handle, seq, st), "mkv_seq_reset")
 
     def copy(self, src, dst, stream=None):
-        st = None if self.host_only else self._stream(stream)
+        st = self._stream(stream)
         _check(lib().mkv_seq_copy(self.handle, src, dst, st), "mkv_seq_copy")
 
     def fork(self, src_ids, dst_ids, n_tokens=None, stream=None):
@@ -427,7 +425,7 @@ class Pool:
         n, nn, _n = (None, ns, None) if n_tokens is None else _i32_list(n_tokens)
         if nd != ns or nn != ns:
             raise ValueError("src_ids, dst_ids and n_tokens must have the same length")
-        st = None if self.host_only else self._stream(stream)
+        st = self._stream(stream)
         _check(lib().mkv_seq_fork(self.handle, s, d, n, ns, st), "mkv_seq_fork")
 
     def truncate(self, seq_ids, n_tokens, stream=None):
@@ -436,20 +434,20 @@ class Pool:
         n, nn, _n = _i32_list(n_tokens)
         if nn != ns:
             raise ValueError("seq_ids and n_tokens must have the same length")
-        st = None if self.host_only else self._stream(stream)
+        st = self._stream(stream)
         _check(lib().mkv_seq_truncate(self.handle, s, n, ns, st), "mkv_seq_truncate")
 
     def free(self, seq_ids, stream=None):
         """Free every page of several sequences (mkv_seq_free)."""
         s, ns, _s = _i32_list(seq_ids)
-        st = None if self.host_only else self._stream(stream)
+        st = self._stream(stream)
         _check(lib().mkv_seq_free(self.handle, s, ns, st), "mkv_seq_free")
 
     def compact(self, stream=None):
         """Move pages so that the slots in use are the first ones of each slab's order; returns
         the number of pages moved (mkv_pool_compact)."""
         n = ctypes.c_int32(0)
-        st = None if self.host_only else self._stream(stream)
+        st = self._stream(stream)
         _check(lib().mkv_pool_compact(self.handle, ctypes.byref(n), st), "mkv_pool_compact")
         return n.value
 
@@ -465,10 +463,10 @@ class Pool:
         shape = (ctx, self.Hkv, self.D)
         k_out = torch.empty(shape, dtype=torch.float32, device=dev) if k_out is None else k_out
         v_out = torch.empty(shape, dtype=torch.float32, device=dev) if v_out is None else v_out
-        kp = _dev_ptr(k_out, torch.float32, "k_out")
-        vp = _dev_ptr(v_out, torch.float32, "v_out")
+        kp = _dev_ptr(k_out, torch.float32, "k_out", self.device_index)
+        vp = _dev_ptr(v_out, torch.float32, "v_out", self.device_index)
         cap = min(k_out.numel(), v_out.numel()) // (self.Hkv * self.D)
-        _check(lib().mkv_materialise_kv(self.handle, seq, kp, vp, cap, _stream_ptr(stream)),
+        _check(lib().mkv_materialise_kv(self.handle, seq, kp, vp, cap, self._stream(stream)),
                "mkv_materialise_kv")
         return k_out, v_out
 
@@ -491,7 +489,7 @@ class Pool:
         nb = self.slot_bytes((entry >> 30) & 3)  # format tag (a BF16 entry is negative)
         buf = np.zeros(nb, dtype=np.uint8)
         _check(lib().mkv_read_slot(self.handle, entry, buf.ctypes.data_as(_P), nb,
-                                   _stream_ptr(stream)), "mkv_read_slot")
+                                   self._stream(stream)), "mkv_read_slot")
         return buf
 
     def stats(self):
@@ -505,7 +503,7 @@ class Pool:
 
     def device_status(self, stream=None):
         """Raise MkvError if a kernel flagged an invalid entry/input or a timed-out wait."""
-        _check(lib().mkv_get_device_status(self.handle, _stream_ptr(stream)), "mkv_get_device_status")
+        _check(lib().mkv_get_device_status(self.handle, self._stream(stream)), "mkv_get_device_status")
 
     def timing(self, enable=True):
         _check(lib().mkv_timing_enable(self.handle, 1 if enable else 0), "mkv_timing_enable")

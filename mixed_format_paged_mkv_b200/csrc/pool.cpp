@@ -281,12 +281,14 @@ bool rows_overlap(const RowSpan& a, const RowSpan& b, int64_t rows) {
   return d < a.width * 2 || step - d < b.width * 2;
 }
 
-// Makes the pool's device current for the calls that take tensors of their own.
+// Makes the device of the pool's buffers current while a call uses it: launches, copies, events and
+// the kernels' occupancy all belong to one device.
 struct DeviceGuard {
   int before = 0;
   bool moved = false;
-  explicit DeviceGuard(int device) {
-    moved = cudaGetDevice(&before) == cudaSuccess && before != device && cudaSetDevice(device) == cudaSuccess;
+  explicit DeviceGuard(const mkv_pool* p) {
+    if (p->host_only) return;
+    moved = cudaGetDevice(&before) == cudaSuccess && before != p->device && cudaSetDevice(p->device) == cudaSuccess;
   }
   ~DeviceGuard() {
     if (moved) cudaSetDevice(before);
@@ -723,7 +725,7 @@ int device_op(mkv_pool_t p, const char* what, F&& f) {
   }
   if (p->fail_after > 0) --p->fail_after;
   if (p->host_only) return MKV_OK;
-  const DeviceGuard guard(p->device);
+  const DeviceGuard guard(p);
   ++p->launches;
   const cudaError_t e = f();
   return e == cudaSuccess ? MKV_OK : cuda_fail(e, what);
@@ -842,7 +844,8 @@ int mkv_pool_create(const mkv_pool_config* cfg, void* fp8_slab, void* tq3_slab,
     cudaError_t e = cudaGetDevice(&dev);
     cudaPointerAttributes at{};
     p->device = cudaPointerGetAttributes(&at, fp8_slab) == cudaSuccess && at.type == cudaMemoryTypeDevice ? at.device : dev;
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->sm_count, cudaDevAttrMultiProcessorCount, dev);
+    const DeviceGuard guard(p);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->sm_count, cudaDevAttrMultiProcessorCount, p->device);
     if (e == cudaSuccess)
       e = cudaMemsetAsync(d_tables, 0xFF, static_cast<size_t>(cfg->max_seqs) * cfg->max_pages_per_seq * 4, 0);
     if (e == cudaSuccess) e = cudaMemsetAsync(d_status, 0, status_bytes(*cfg), 0);
@@ -1084,6 +1087,7 @@ int mkv_decode_workspace_bytes(mkv_pool_t p, const int32_t* seq_ids, int32_t n_s
                                int32_t q_len, int32_t Hq, size_t* bytes) {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (!bytes) return fail(MKV_ERR_INVALID_ARG, "bytes is NULL");
+  const DeviceGuard guard(p);
   DecodePlan plan;
   if (int e = plan_decode(p, seq_ids, n_seqs, q_len, Hq, &plan)) return e;
   *bytes = plan.bytes;
@@ -1095,6 +1099,7 @@ int mkv_decode_plan(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32_
                     int32_t* ctas_per_wave) {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (!n_units || cap < 0) return fail(MKV_ERR_INVALID_ARG, "n_units is NULL or cap < 0");
+  const DeviceGuard guard(p);
   DecodePlan plan;
   if (int e = plan_decode(p, seq_ids, n_seqs, q_len, Hq, &plan)) return e;
   const int64_t nu = static_cast<int64_t>(plan.unit.size());
@@ -1125,6 +1130,7 @@ int mkv_decode_attention(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, i
                          void* workspace, size_t ws_bytes, void* stream) {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (p->host_only) return fail(MKV_ERR_INVALID_ARG, "host-only pool cannot decode");
+  const DeviceGuard guard(p);
   DecodePlan plan;
   if (int e = plan_decode(p, seq_ids, n_seqs, q_len, Hq, &plan)) return e;
   if (!std::isfinite(sm_scale)) return fail(MKV_ERR_INVALID_ARG, "sm_scale is not finite");
@@ -1204,6 +1210,7 @@ int mkv_decode_attention_noalloc(mkv_pool_t p, const int32_t* seq_ids, int32_t n
                                  float* out, void* stream) {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (p->host_only) return fail(MKV_ERR_INVALID_ARG, "host-only pool cannot decode");
+  const DeviceGuard guard(p);
   if (n_seqs < 0 || (n_seqs > 0 && !seq_ids)) return fail(MKV_ERR_INVALID_ARG, "bad sequence list");
   if (n_seqs > p->cfg.max_seqs)
     return fail(MKV_ERR_INVALID_ARG, "at most max_seqs (%d) sequences per decode call", p->cfg.max_seqs);
@@ -1378,7 +1385,7 @@ int mkv_rope(mkv_pool_t p, int64_t rows, const int32_t* positions, int32_t n_axe
   prm.next = interleaved ? 1 : 0;
   prm.vec = (bits & 15) == 0 && n_freq % 8 == 0 ? 1 : 0;
   for (int32_t i = 0; axis_of && i < n_freq; ++i) prm.axis[i] = static_cast<uint8_t>(axis_of[i]);
-  const DeviceGuard guard(p->device);
+  const DeviceGuard guard(p);
   const cudaError_t e = launch_rope(prm, as_stream(stream));
   ++p->launches;
   if (e != cudaSuccess) return cuda_fail(e, "rope launch");
@@ -1426,7 +1433,7 @@ int mkv_prompt_attention(mkv_pool_t p, const int32_t* n_tokens, int32_t n_prompt
   for (int32_t i = 0; i < n_prompts; row += n_tokens[i++])
     if (n_tokens[i] > 0) seqs.push_back({row, n_tokens[i], 0});
   std::stable_sort(seqs.begin(), seqs.end(), [](const PromptSeq& a, const PromptSeq& b) { return a.len > b.len; });
-  const DeviceGuard guard(p->device);
+  const DeviceGuard guard(p);
   std::unique_ptr<PromptParams> prm(new PromptParams);
   prm->out = static_cast<uint16_t*>(out_bf16);
   prm->v = static_cast<const uint16_t*>(v_bf16);
@@ -1469,6 +1476,7 @@ int mkv_selftest_wait(mkv_pool_t p, int64_t limit_ns, void* stream) {
   if (p->host_only) return fail(MKV_ERR_INVALID_ARG, "host-only pool has no device");
   if (limit_ns < 0 || limit_ns > 2000000000LL)
     return fail(MKV_ERR_INVALID_ARG, "limit must be in [0, 2 s]");
+  const DeviceGuard guard(p);
   cudaError_t e = launch_wait_selftest(p->d_status, static_cast<uint64_t>(limit_ns), as_stream(stream));
   ++p->launches;
   if (e != cudaSuccess) return cuda_fail(e, "self-test launch");
@@ -1480,6 +1488,7 @@ int mkv_selftest_tc_logits(mkv_pool_t p, const void* a_f16, const void* q_f16, f
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (p->host_only) return fail(MKV_ERR_INVALID_ARG, "host-only pool has no device");
   if (!a_f16 || !q_f16 || !d_out) return fail(MKV_ERR_INVALID_ARG, "a/q/d is NULL");
+  const DeviceGuard guard(p);
   cudaError_t e = launch_tc_logits_selftest(a_f16, q_f16, d_out, p->d_status, as_stream(stream));
   ++p->launches;
   if (e != cudaSuccess) return cuda_fail(e, "tensor-memory self-test launch");
@@ -1639,6 +1648,7 @@ int mkv_materialise_kv(mkv_pool_t p, int32_t seq, float* k_out, float* v_out,
   prm.fp8_slots = p->cfg.fp8_slots;
   prm.tq3_slots = p->cfg.tq3_slots;
   prm.page_fmt = p->page_fmt;
+  const DeviceGuard guard(p);
   cudaError_t e = launch_materialise(prm, as_stream(stream));
   ++p->launches;
   if (e != cudaSuccess) return cuda_fail(e, "materialise launch");
@@ -1996,6 +2006,7 @@ int mkv_read_slot(mkv_pool_t p, int32_t entry, void* host_out, size_t cap, void*
   if (!host_out || cap < static_cast<size_t>(b)) return fail(MKV_ERR_INVALID_ARG, "output buffer too small");
   const uint8_t* src = (f == MKV_FMT_TQ3 ? p->tq3_slab : p->fp8_slab) + slot * b;
   cudaStream_t st = as_stream(stream);
+  const DeviceGuard guard(p);
   cudaError_t e = cudaMemcpyAsync(host_out, src, b, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(e, "read slot");
@@ -2019,6 +2030,7 @@ int mkv_get_device_status(mkv_pool_t p, void* stream) {
   if (p->host_only) return ok();
   cudaStream_t st = as_stream(stream);
   int32_t h = 0;
+  const DeviceGuard guard(p);
   cudaError_t e = cudaStreamSynchronize(st);
   if (e == cudaSuccess) e = cudaMemcpy(&h, p->d_status, 4, cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaMemset(p->d_status, 0, 4);
