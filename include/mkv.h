@@ -55,7 +55,9 @@
  * launches may, when a later one fails, have written pages into slots that stay free and, for
  * an append, have re-encoded existing partial pages (rescale-on-grow): reset the sequences of
  * such a call.  A split demotion publishes no table entry before all its pages are written.
- * When several arguments of a
+ * A call that runs out of host
+ * memory returns INVALID_ARG ("out of host memory") and leaves the pool unchanged (mkv_pool_compact:
+ * one slab may be done); no C++ exception crosses this interface.  When several arguments of a
  * call taking a sequence list are wrong, an out-of-range id (BAD_SEQ) is reported before any
  * other argument error (INVALID_ARG), and those before a capacity error (OUT_OF_PAGES).  Device-side checks (bad
  * table entries, bounded waits that ran out) are recorded in the caller's status word and

@@ -15,7 +15,6 @@
 #include <limits>
 #include <memory>
 #include <new>
-#include <string>
 #include <unordered_map>
 #include <vector>
 
@@ -27,21 +26,29 @@ using namespace mkv;
 
 namespace {
 
-thread_local std::string g_last_error;
+thread_local char g_last_error[512];  // (no allocation: "out of host memory" is reported here too)
 
 int fail(int code, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return code;
 }
 
 int ok() {
-  g_last_error.clear();
+  g_last_error[0] = 0;
   return MKV_OK;
+}
+
+// A call that allocates catches bad_alloc: nothing is thrown through the C ABI.  It allocates before it
+// takes a slot or issues a launch, so that one that runs out of memory leaves the pool as it was.
+int out_of_memory() { return fail(MKV_ERR_INVALID_ARG, "out of host memory"); }
+
+// Room for n elements, growing by half as much again at least (appends come one token at a time).
+template <class T>
+void grow(std::vector<T>* v, size_t n) {
+  if (n > v->capacity()) v->reserve(std::max(n, v->capacity() + v->capacity() / 2));
 }
 
 int cuda_fail(cudaError_t e, const char* what) {
@@ -116,6 +123,13 @@ struct Seq {
   std::vector<uint8_t> prot;      // protected flag per logical page
   int32_t ctx = 0;
   int32_t n3 = 0;
+  // Room for the pages [before, after) of the written format (an append or a branch adds no others).
+  void grow(size_t before, size_t after) {
+    if (after <= before) return;
+    ::grow(&table, after);
+    ::grow(&prot, after);
+    ::grow(&fp8_pages, fp8_pages.size() + after - before);
+  }
   void clear() {  // (the lists keep their memory: branches come and go with every step)
     table.clear();
     fp8_pages.clear();
@@ -798,7 +812,7 @@ cudaEvent_t get_event(mkv_pool_t p) {
 // ====================================================================== C ABI
 extern "C" {
 
-const char* mkv_last_error(void) { return g_last_error.c_str(); }
+const char* mkv_last_error(void) { return g_last_error; }
 
 int mkv_pool_required_bytes(const mkv_pool_config* cfg, size_t* fp8_slab, size_t* tq3_slab,
                             size_t* tables, size_t* status) {
@@ -812,7 +826,7 @@ int mkv_pool_required_bytes(const mkv_pool_config* cfg, size_t* fp8_slab, size_t
 }
 
 int mkv_pool_create(const mkv_pool_config* cfg, void* fp8_slab, void* tq3_slab,
-                    int32_t* d_tables, int32_t* d_status, mkv_pool_t* out) {
+                    int32_t* d_tables, int32_t* d_status, mkv_pool_t* out) try {
   if (int e = validate_config(cfg)) return e;
   if (!out) return fail(MKV_ERR_INVALID_ARG, "out is NULL");
   const bool host_only = (cfg->flags & MKV_POOL_HOST_ONLY) != 0;
@@ -826,7 +840,8 @@ int mkv_pool_create(const mkv_pool_config* cfg, void* fp8_slab, void* tq3_slab,
                         reinterpret_cast<uintptr_t>(d_tables) | reinterpret_cast<uintptr_t>(d_status);
     if (a & 255) return fail(MKV_ERR_INVALID_ARG, "device buffers must be 256-byte aligned");
   }
-  mkv_pool* p = new mkv_pool();
+  std::unique_ptr<mkv_pool> owner(new mkv_pool());
+  mkv_pool* p = owner.get();
   p->cfg = *cfg;
   p->host_only = host_only;
   p->fp8_slab = static_cast<uint8_t*>(fp8_slab);
@@ -850,13 +865,12 @@ int mkv_pool_create(const mkv_pool_config* cfg, void* fp8_slab, void* tq3_slab,
       e = cudaMemsetAsync(d_tables, 0xFF, static_cast<size_t>(cfg->max_seqs) * cfg->max_pages_per_seq * 4, 0);
     if (e == cudaSuccess) e = cudaMemsetAsync(d_status, 0, status_bytes(*cfg), 0);
     if (e == cudaSuccess) e = cudaStreamSynchronize(0);
-    if (e != cudaSuccess) {
-      delete p;
-      return cuda_fail(e, "pool init");
-    }
+    if (e != cudaSuccess) return cuda_fail(e, "pool init");
   }
-  *out = p;
+  *out = owner.release();
   return ok();
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 void mkv_pool_destroy(mkv_pool_t p) {
@@ -867,7 +881,7 @@ void mkv_pool_destroy(mkv_pool_t p) {
   delete p;
 }
 
-int mkv_pool_set_slot_order(mkv_pool_t p, int32_t fmt, const int32_t* order, int32_t n) {
+int mkv_pool_set_slot_order(mkv_pool_t p, int32_t fmt, const int32_t* order, int32_t n) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (fmt != MKV_FMT_FP8 && fmt != MKV_FMT_TQ3 && fmt != MKV_FMT_BF16)
     return fail(MKV_ERR_INVALID_ARG, "bad format");
@@ -881,15 +895,17 @@ int mkv_pool_set_slot_order(mkv_pool_t p, int32_t fmt, const int32_t* order, int
   }
   a.set_order(order);
   return ok();
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 int mkv_append_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_new, int32_t n_seqs,
-                  const void* k_bf16, const void* v_bf16, void* stream) {
+                  const void* k_bf16, const void* v_bf16, void* stream) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (n_seqs < 0 || (n_seqs > 0 && (!seq_ids || !n_new)))
     return fail(MKV_ERR_INVALID_ARG, "bad sequence list");
   const int32_t MP = p->cfg.max_pages_per_seq;
-  int64_t need = 0, rows = 0;
+  int64_t need = 0, rows = 0, writes = 0;
   if (int e = check_seq_list(p, seq_ids, n_seqs, n_new)) return e;
   for (int32_t i = 0; i < n_seqs; ++i) {
     const Seq& s = p->seqs[seq_ids[i]];
@@ -899,6 +915,7 @@ int mkv_append_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_new, in
                   static_cast<long long>(pages_after), MP);
     need += pages_after - static_cast<int64_t>(s.table.size());
     rows += n_new[i];
+    writes += n_new[i] > 0 ? pages_after - s.ctx / kPageTokens : 0;
   }
   if (need > p->alloc[0].n_free)
     return fail(MKV_ERR_OUT_OF_PAGES, "FP8 slab has %d free slots, %lld needed", p->alloc[0].n_free,
@@ -911,6 +928,13 @@ int mkv_append_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_new, in
   std::vector<int32_t> taken;      // new slots, sequences in order, pages ascending
   std::vector<size_t> first_new(n_seqs);
   std::vector<AppendDesc> descs;
+  std::unique_ptr<AppendParams> prm(writes > 0 ? new AppendParams : nullptr);
+  taken.reserve(need);
+  descs.reserve(writes);
+  for (int32_t i = 0; i < n_seqs; ++i) {
+    Seq& s = p->seqs[seq_ids[i]];
+    s.grow(s.table.size(), (static_cast<size_t>(s.ctx) + n_new[i] + kPageTokens - 1) / kPageTokens);
+  }
   int32_t row = 0;
   for (int32_t i = 0; i < n_seqs; ++i) {
     const Seq& s = p->seqs[seq_ids[i]];
@@ -935,7 +959,6 @@ int mkv_append_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_new, in
   // ---- launch
   int rc = MKV_OK;
   if (!descs.empty()) {
-    AppendParams* prm = new AppendParams;
     prm->fp8_slab = p->fp8_slab;
     prm->tables = p->d_tables;
     prm->status = p->d_status;
@@ -951,7 +974,6 @@ int mkv_append_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_new, in
       std::memcpy(prm->desc, descs.data() + b, m * sizeof(AppendDesc));
       rc = device_op(p, "append launch", [&] { return launch_append(*prm, as_stream(stream)); });
     }
-    delete prm;
   }
   if (rc != MKV_OK) {
     for (auto it = taken.rbegin(); it != taken.rend(); ++it) p->alloc[0].give(*it);
@@ -969,6 +991,8 @@ int mkv_append_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_new, in
     s.ctx += n_new[i];
   }
   return ok();
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 int mkv_set_protected(mkv_pool_t p, int32_t seq, int32_t page, int32_t flag) {
@@ -982,7 +1006,7 @@ int mkv_set_protected(mkv_pool_t p, int32_t seq, int32_t page, int32_t flag) {
 }
 
 int mkv_demote_pages(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32_t window,
-                     int32_t* n_demoted, void* stream) {
+                     int32_t* n_demoted, void* stream) try {
   if (n_demoted) *n_demoted = 0;
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (n_seqs < 0 || (n_seqs > 0 && !seq_ids)) return fail(MKV_ERR_INVALID_ARG, "bad sequence list");
@@ -1021,15 +1045,16 @@ int mkv_demote_pages(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32
   }
   if (static_cast<int64_t>(descs.size()) > p->alloc[1].n_free)
     return fail(MKV_ERR_OUT_OF_PAGES, "TQ3 slab has %d free slots, %zu needed", p->alloc[1].n_free, descs.size());
+  // (an entry per listed page: more entries than pages where sequences share one)
+  const bool single = descs.size() <= static_cast<size_t>(kDemoteMaxDesc) && descs.size() == work.size();
+  std::unique_ptr<DemoteParams> prm(descs.empty() ? nullptr : new DemoteParams);
+  std::unique_ptr<RetagParams> rp(single ? nullptr : new RetagParams);
   for (DemoteDesc& d : descs) d.dst_slot = p->alloc[1].take();
   // ---- launch: one launch writes the pages and publishes their table entries; a call that
   // needs several launches publishes no entry until every page is written (retag launches
   // last), so a failed launch never leaves a device entry naming an unwritten page
   int rc = MKV_OK;
   if (!descs.empty()) {
-    // (an entry per listed page: more entries than pages where sequences share one)
-    const bool single = descs.size() <= static_cast<size_t>(kDemoteMaxDesc) && descs.size() == work.size();
-    DemoteParams* prm = new DemoteParams;
     prm->fp8_slab = p->fp8_slab;
     prm->tq3_slab = p->tq3_slab;
     prm->tables = p->d_tables;
@@ -1044,9 +1069,7 @@ int mkv_demote_pages(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32
       std::memcpy(prm->desc, descs.data() + b, m * sizeof(DemoteDesc));
       rc = device_op(p, "demote launch", [&] { return launch_demote(*prm, as_stream(stream)); });
     }
-    delete prm;
     if (!single && rc == MKV_OK) {
-      RetagParams* rp = new RetagParams;
       rp->tables = p->d_tables;
       for (size_t b = 0; b < work.size() && rc == MKV_OK; b += kRetagMax) {
         const size_t m = std::min<size_t>(kRetagMax, work.size() - b);
@@ -1057,7 +1080,6 @@ int mkv_demote_pages(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32
         }
         rc = device_op(p, "retag launch", [&] { return launch_retag(*rp, as_stream(stream)); });
       }
-      delete rp;
     }
   }
   if (rc != MKV_OK) {
@@ -1081,10 +1103,12 @@ int mkv_demote_pages(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32
   for (int32_t k : to) p->alloc[0].give(descs[k].src_slot);
   if (n_demoted) *n_demoted = static_cast<int32_t>(work.size());
   return ok();
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 int mkv_decode_workspace_bytes(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs,
-                               int32_t q_len, int32_t Hq, size_t* bytes) {
+                               int32_t q_len, int32_t Hq, size_t* bytes) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (!bytes) return fail(MKV_ERR_INVALID_ARG, "bytes is NULL");
   const DeviceGuard guard(p);
@@ -1092,11 +1116,13 @@ int mkv_decode_workspace_bytes(mkv_pool_t p, const int32_t* seq_ids, int32_t n_s
   if (int e = plan_decode(p, seq_ids, n_seqs, q_len, Hq, &plan)) return e;
   *bytes = plan.bytes;
   return ok();
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 int mkv_decode_plan(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32_t q_len,
                     int32_t Hq, int32_t* units_out, int32_t cap, int32_t* n_units,
-                    int32_t* ctas_per_wave) {
+                    int32_t* ctas_per_wave) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (!n_units || cap < 0) return fail(MKV_ERR_INVALID_ARG, "n_units is NULL or cap < 0");
   const DeviceGuard guard(p);
@@ -1123,11 +1149,13 @@ int mkv_decode_plan(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32_
     cta0 += ld.n_ctas;
   }
   return ok();
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 int mkv_decode_attention(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, int32_t q_len,
                          const void* q_bf16, int32_t Hq, float sm_scale, float* out,
-                         void* workspace, size_t ws_bytes, void* stream) {
+                         void* workspace, size_t ws_bytes, void* stream) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (p->host_only) return fail(MKV_ERR_INVALID_ARG, "host-only pool cannot decode");
   const DeviceGuard guard(p);
@@ -1142,7 +1170,7 @@ int mkv_decode_attention(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, i
     return fail(MKV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", ws_bytes, plan.bytes);
   cudaStream_t st = as_stream(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  DecodeParams* prm = new DecodeParams;
+  std::unique_ptr<DecodeParams> prm(new DecodeParams);
   prm->fp8_slab = p->fp8_slab;
   prm->tq3_slab = p->tq3_slab;
   prm->tables = p->d_tables;
@@ -1165,9 +1193,12 @@ int mkv_decode_attention(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, i
   prm->logit_scale = sm_scale * 1.4426950408889634f;
   TimingRec rec{};
   bool timed = p->timing;
-  if (timed)
+  if (timed) {
+    grow(&p->timing_recs, p->timing_recs.size() + 1);
+    grow(&p->spare_events, p->spare_events.size() + 3);
     for (auto& e : rec.ev)
       if (!(e = get_event(p))) timed = false;
+  }
   cudaError_t err = timed ? cudaEventRecord(rec.ev[0], st) : cudaSuccess;
   // one launch (partial grids + merge) per group of whole sequences
   for (size_t li = 0; li < plan.launch.size() && err == cudaSuccess; ++li) {
@@ -1178,7 +1209,7 @@ int mkv_decode_attention(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, i
       prm->unit[k] = plan.unit[ld.u0 + k];
       prm->unit[k].seq = static_cast<uint8_t>(plan.pos[ld.u0 + k] - ld.s0);
     }
-    if (!fill_cta_table(prm, plan.cta.data() + ld.u0, nu, ld.n_ctas)) {
+    if (!fill_cta_table(prm.get(), plan.cta.data() + ld.u0, nu, ld.n_ctas)) {
       err = cudaErrorInvalidValue;
       break;
     }
@@ -1193,13 +1224,14 @@ int mkv_decode_attention(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, i
     if (err == cudaSuccess) err = launch_merge(*prm, st), ++p->launches;
   }
   if (timed && err == cudaSuccess) err = cudaEventRecord(rec.ev[2], st);
-  delete prm;
   if (timed) {
     if (err == cudaSuccess) p->timing_recs.push_back(rec);
     else for (auto e : rec.ev) p->spare_events.push_back(e);
   }
   if (err != cudaSuccess) return cuda_fail(err, "decode launch");
   return ok();
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 // Decode with the library's static partial-state scratch instead of a caller workspace.  Same
@@ -1468,7 +1500,7 @@ int mkv_prompt_attention(mkv_pool_t p, const int32_t* n_tokens, int32_t n_prompt
   }
   return ok();
 } catch (const std::bad_alloc&) {
-  return fail(MKV_ERR_INVALID_ARG, "out of host memory");
+  return out_of_memory();
 }
 
 int mkv_selftest_wait(mkv_pool_t p, int64_t limit_ns, void* stream) {
@@ -1497,7 +1529,7 @@ int mkv_selftest_tc_logits(mkv_pool_t p, const void* a_f16, const void* q_f16, f
 
 int mkv_prefill_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_tokens, int32_t n_seqs,
                    const void* k_bf16, const void* v_bf16, int32_t anchor_window_tokens,
-                   void* stream) {
+                   void* stream) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (n_seqs < 0 || (n_seqs > 0 && (!seq_ids || !n_tokens)))
     return fail(MKV_ERR_INVALID_ARG, "bad sequence list");
@@ -1536,6 +1568,20 @@ int mkv_prefill_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_tokens
   std::vector<int32_t> taken[2];   // slots per format, in the order taken
   std::vector<AppendDesc> fp8_descs;
   std::vector<PackDesc> tq3_descs;
+  std::unique_ptr<AppendParams> ap(need[0] > 0 ? new AppendParams : nullptr);
+  std::unique_ptr<PackParams> pp(need[1] > 0 ? new PackParams : nullptr);
+  for (int f = 0; f < 2; ++f) taken[f].reserve(need[f]);
+  fp8_descs.reserve(need[0]);
+  tq3_descs.reserve(need[1]);
+  for (int32_t i = 0; i < n_seqs; ++i) {
+    Seq& s = p->seqs[seq_ids[i]];
+    const int64_t pages = (static_cast<int64_t>(n_tokens[i]) + kPageTokens - 1) / kPageTokens;
+    int64_t fp8 = 0;
+    for (int64_t pg = 0; pg < pages; ++pg) fp8 += direct(pg, n_tokens[i]) ? 0 : 1;
+    grow(&s.table, pages);
+    grow(&s.prot, pages);
+    grow(&s.fp8_pages, fp8);
+  }
   int32_t row = 0;
   for (int32_t i = 0; i < n_seqs; ++i) {
     const int32_t n = n_tokens[i], pages = (n + kPageTokens - 1) / kPageTokens;
@@ -1564,7 +1610,6 @@ int mkv_prefill_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_tokens
   cudaStream_t st = as_stream(stream);
   int rc = MKV_OK;
   if (!fp8_descs.empty()) {
-    AppendParams* ap = new AppendParams;
     ap->fp8_slab = p->fp8_slab;
     ap->tables = p->d_tables;
     ap->status = p->d_status;
@@ -1580,10 +1625,8 @@ int mkv_prefill_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_tokens
       std::memcpy(ap->desc, fp8_descs.data() + b, m * sizeof(AppendDesc));
       rc = device_op(p, "prefill launch", [&] { return launch_append(*ap, st); });
     }
-    delete ap;
   }
   if (!tq3_descs.empty() && rc == MKV_OK) {
-    PackParams* pp = new PackParams;
     pp->k = static_cast<const uint16_t*>(k_bf16);
     pp->v = static_cast<const uint16_t*>(v_bf16);
     pp->tq3_slab = p->tq3_slab;
@@ -1598,7 +1641,6 @@ int mkv_prefill_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_tokens
       std::memcpy(pp->desc, tq3_descs.data() + b, m * sizeof(PackDesc));
       rc = device_op(p, "prefill launch", [&] { return launch_pack(*pp, st); });
     }
-    delete pp;
   }
   if (rc != MKV_OK) {
     for (int f = 0; f < 2; ++f)
@@ -1620,6 +1662,8 @@ int mkv_prefill_kv(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_tokens
     s.ctx = n;
   }
   return ok();
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 int mkv_materialise_kv(mkv_pool_t p, int32_t seq, float* k_out, float* v_out,
@@ -1655,7 +1699,7 @@ int mkv_materialise_kv(mkv_pool_t p, int32_t seq, float* k_out, float* v_out,
   return ok();
 }
 
-int mkv_seq_copy(mkv_pool_t p, int32_t src, int32_t dst, void* stream) {
+int mkv_seq_copy(mkv_pool_t p, int32_t src, int32_t dst, void* stream) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
   if (int e = check_seq(p, src)) return e;
   if (int e = check_seq(p, dst)) return e;
@@ -1692,6 +1736,8 @@ int mkv_seq_copy(mkv_pool_t p, int32_t src, int32_t dst, void* stream) {
   }
   p->seqs[dst] = std::move(d);
   return ok();
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 int mkv_seq_fork(mkv_pool_t p, const int32_t* src_ids, const int32_t* dst_ids, const int32_t* n_tokens,
@@ -1723,6 +1769,21 @@ int mkv_seq_fork(mkv_pool_t p, const int32_t* src_ids, const int32_t* dst_ids, c
   // ---- stage and launch: the shared pages' entries are copied on the device, a partial last page
   // gets a slot of its own (only full pages are ever shared, so appends never write a shared page)
   std::vector<int32_t> taken;
+  taken.reserve(need);
+  std::vector<int32_t> by_src(n_forks);  // list positions, sources together
+  size_t longest = 0;
+  for (int32_t i = 0; i < n_forks; ++i) {
+    by_src[i] = i;
+    const Seq& s = p->seqs[src_ids[i]];
+    longest = std::max(longest, s.table.size());
+    const int32_t at = n_tokens ? n_tokens[i] : s.ctx, pages = (at + kPageTokens - 1) / kPageTokens;
+    Seq& d = p->seqs[dst_ids[i]];
+    grow(&d.table, pages);
+    grow(&d.prot, pages);
+    grow(&d.fp8_pages, std::lower_bound(s.fp8_pages.begin(), s.fp8_pages.end(), pages) - s.fp8_pages.begin());
+  }
+  std::sort(by_src.begin(), by_src.end(), [&](int32_t x, int32_t y) { return src_ids[x] < src_ids[y]; });
+  std::vector<int32_t> ends(longest + 1, 0);
   PageOps ops(p, "fork launch", stream);
   int rc = MKV_OK;
   for (int32_t i = 0; i < n_forks && rc == MKV_OK; ++i) {
@@ -1740,12 +1801,9 @@ int mkv_seq_fork(mkv_pool_t p, const int32_t* src_ids, const int32_t* dst_ids, c
     return rc;
   }
   // ---- commit: a shared page's count grows once by all branches of its source that reach it
-  std::vector<int32_t> by_src(n_forks);
-  for (int32_t i = 0; i < n_forks; ++i) by_src[i] = i;
-  std::sort(by_src.begin(), by_src.end(), [&](int32_t x, int32_t y) { return src_ids[x] < src_ids[y]; });
   for (int32_t a = 0, b = 0; a < n_forks; a = b) {
     const Seq& s = p->seqs[src_ids[by_src[a]]];
-    std::vector<int32_t> ends(s.table.size() + 1, 0);  // branches with that many full pages
+    std::fill_n(ends.begin(), s.table.size() + 1, 0);  // branches with that many full pages
     int32_t reach = 0;
     for (b = a; b < n_forks && src_ids[by_src[b]] == src_ids[by_src[a]]; ++b, ++reach)
       ++ends[(n_tokens ? n_tokens[by_src[b]] : s.ctx) / kPageTokens];
@@ -1771,7 +1829,7 @@ int mkv_seq_fork(mkv_pool_t p, const int32_t* src_ids, const int32_t* dst_ids, c
   }
   return ok();
 } catch (const std::bad_alloc&) {
-  return fail(MKV_ERR_INVALID_ARG, "out of host memory");
+  return out_of_memory();
 }
 
 int mkv_seq_truncate(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_tokens, int32_t n_seqs,
@@ -1787,12 +1845,15 @@ int mkv_seq_truncate(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_toke
     return n_tokens[i] < s.ctx && n_tokens[i] % kPageTokens ? n_tokens[i] / kPageTokens : -1;
   };
   int64_t need = 0;
+  size_t n_cuts = 0, n_dropped = 0;
   for (int32_t i = 0; i < n_seqs; ++i) {
     const Seq& s = p->seqs[seq_ids[i]];
     if (n_tokens[i] > s.ctx)
       return fail(MKV_ERR_INVALID_ARG, "sequence %d has %d tokens < %d", seq_ids[i], s.ctx, n_tokens[i]);
+    n_dropped += s.table.size() - (n_tokens[i] + kPageTokens - 1) / kPageTokens;
     const int32_t pg = cut_page(i);
     if (pg < 0) continue;
+    ++n_cuts;
     if (fmt_of(s.table[pg]) == MKV_FMT_TQ3)
       return fail(MKV_ERR_UNSUPPORTED, "%d tokens end inside a TQ3 page of sequence %d", n_tokens[i], seq_ids[i]);
     need += p->alloc[0].refs[slot_of(s.table[pg])] > 1 ? 1 : 0;
@@ -1803,10 +1864,12 @@ int mkv_seq_truncate(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_toke
   // ---- stage and launch
   struct Cut { int32_t i, old_slot, new_slot; };  // (old == new: the page is the sequence's own)
   std::vector<Cut> cuts;
+  cuts.reserve(n_cuts);
   PageOps ops(p, "truncate launch", stream);
   // commit of the sequences [a, b) of the list, whose launches were issued
   size_t next = 0;
   std::vector<int32_t> dropped;
+  dropped.reserve(n_dropped + need);
   auto commit = [&](int32_t a, int32_t b) {
     for (int32_t i = a; i < b; ++i) {
       Seq& s = p->seqs[seq_ids[i]];
@@ -1853,7 +1916,7 @@ int mkv_seq_truncate(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_toke
   for (int32_t e : dropped) p->alloc[slab_of(fmt_of(e))].give(slot_of(e));
   return rc == MKV_OK ? ok() : rc;
 } catch (const std::bad_alloc&) {
-  return fail(MKV_ERR_INVALID_ARG, "out of host memory");
+  return out_of_memory();
 }
 
 int mkv_seq_free(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, void* stream) try {
@@ -1898,7 +1961,7 @@ int mkv_seq_free(mkv_pool_t p, const int32_t* seq_ids, int32_t n_seqs, void* str
   commit(done, n_seqs);
   return ok();
 } catch (const std::bad_alloc&) {
-  return fail(MKV_ERR_INVALID_ARG, "out of host memory");
+  return out_of_memory();
 }
 
 int mkv_pool_compact(mkv_pool_t p, int32_t* n_moved, void* stream) try {
@@ -1970,7 +2033,7 @@ int mkv_pool_compact(mkv_pool_t p, int32_t* n_moved, void* stream) try {
   }
   return rc == MKV_OK ? ok() : rc;
 } catch (const std::bad_alloc&) {
-  return fail(MKV_ERR_INVALID_ARG, "out of host memory");
+  return out_of_memory();
 }
 
 int mkv_get_block_table(mkv_pool_t p, int32_t seq, int32_t* host_out, int32_t cap,
@@ -2046,8 +2109,9 @@ int mkv_timing_enable(mkv_pool_t p, int32_t enable) {
   return ok();
 }
 
-int mkv_timing_read(mkv_pool_t p, double* ms_partial, double* ms_merge, int64_t* calls) {
+int mkv_timing_read(mkv_pool_t p, double* ms_partial, double* ms_merge, int64_t* calls) try {
   if (!valid_pool(p)) return fail(MKV_ERR_INVALID_ARG, "pool is NULL");
+  grow(&p->spare_events, p->spare_events.size() + 3 * p->timing_recs.size());
   double a = 0, b = 0;
   cudaError_t err = cudaSuccess;
   for (auto& r : p->timing_recs) {
@@ -2067,6 +2131,8 @@ int mkv_timing_read(mkv_pool_t p, double* ms_partial, double* ms_merge, int64_t*
   if (ms_merge) *ms_merge = b;
   if (calls) *calls = n;
   return ok();
+} catch (const std::bad_alloc&) {
+  return out_of_memory();
 }
 
 int mkv_set_decode_kernels(mkv_pool_t p, int32_t mode) {

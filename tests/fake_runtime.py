@@ -18,7 +18,11 @@ def build(folder):
     subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-fvisibility=hidden", "-Wl,-Bsymbolic",
                     f"-I{INCLUDE}", f"-I{CSRC}", f"-I{cuda}", os.path.join(CSRC, "pool.cpp"),
                     os.path.join(HERE, "fake_runtime.cpp"), "-o", out], check=True)
-    lib = ctypes.CDLL(out)
+    return load(out)
+
+
+def load(path):
+    lib = ctypes.CDLL(path)
     for name, (res, args) in api.SIGNATURES.items():
         getattr(lib, name).restype, getattr(lib, name).argtypes = res, args
     lib.fake_log.restype = ctypes.c_char_p
