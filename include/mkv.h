@@ -50,7 +50,8 @@
  * thread-local message readable with mkv_last_error().  Host validation runs before any
  * launch; a call that fails validation leaves the pool unchanged.  A call whose launch fails
  * (MKV_ERR_CUDA) leaves the pool's host state -- tables, free slots, lengths, flags -- unchanged
- * too: state changes are staged and committed after the call's last launch.  On the device, a
+ * too: state changes are staged and committed after the call's last launch
+ * (mkv_seq_truncate, mkv_seq_free and mkv_pool_compact: after each launch).  On the device, a
  * call issued as one launch either ran or did not; a call so large that it is split into several
  * launches may, when a later one fails, have written pages into slots that stay free and, for
  * an append, have re-encoded existing partial pages (rescale-on-grow): reset the sequences of
@@ -285,9 +286,9 @@ MKV_API int mkv_seq_fork(mkv_pool_t pool, const int32_t* src_ids, const int32_t*
 /* Roll sequences back to their first n_tokens[i] tokens (rejected speculative tokens): pages past
  * the new end are given up, rows past it in its page become zero (the page's scales stay), after
  * the page was copied to a slot of the sequence's own where others share it.  Slots are taken in
- * list order before any is freed.  A call split over several launches (more than 960 sequences)
- * takes effect launch by launch in list order, so one that fails has rolled back a leading part
- * of the list.  Errors: BAD_SEQ, INVALID_ARG (also n_tokens[i] above the length), UNSUPPORTED
+ * list order before any is freed.  A call split over several launches (more than 850 new ends
+ * inside a page, or more than 960 sequences that give up pages) takes effect launch by launch in
+ * list order, so one that fails has rolled back a leading part of the list.  Errors: BAD_SEQ, INVALID_ARG (also n_tokens[i] above the length), UNSUPPORTED
  * (n_tokens[i] ends inside a TQ3 page), OUT_OF_PAGES (nothing changed), CUDA. */
 MKV_API int mkv_seq_truncate(mkv_pool_t pool, const int32_t* seq_ids, const int32_t* n_tokens,
                              int32_t n_seqs, void* stream);

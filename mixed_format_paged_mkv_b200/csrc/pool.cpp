@@ -1893,14 +1893,14 @@ int mkv_seq_truncate(mkv_pool_t p, const int32_t* seq_ids, const int32_t* n_toke
   int rc = MKV_OK;
   int32_t done = 0;
   for (int32_t i = 0; i < n_seqs && rc == MKV_OK; ++i) {
-    if (!ops.fits(1, 1)) {
+    const Seq& s = p->seqs[seq_ids[i]];
+    const int32_t keep = (n_tokens[i] + kPageTokens - 1) / kPageTokens;
+    const int32_t pages = static_cast<int32_t>(s.table.size()), pg = cut_page(i);
+    if (!ops.fits(pg >= 0 ? 1 : 0, pages > keep ? 1 : 0)) {
       if ((rc = ops.flush()) != MKV_OK) break;
       commit(done, i);
       done = i;
     }
-    const Seq& s = p->seqs[seq_ids[i]];
-    const int32_t keep = (n_tokens[i] + kPageTokens - 1) / kPageTokens;
-    const int32_t pages = static_cast<int32_t>(s.table.size()), pg = cut_page(i);
     if (pages > keep) ops.row({-1, seq_ids[i] * MP + keep, pages - keep});
     if (pg >= 0) {
       const int32_t old_slot = slot_of(s.table[pg]);
