@@ -161,14 +161,18 @@ def _empty_like(t, shape, stream):
 
 
 def _i32_list(xs):
-    """(address, length, owner) of a list's int32 values on the host; the owner keeps them alive."""
+    """(address, length, owner) of a list's int32 values on the host; the owner keeps them alive.
+    Anything but whole numbers that fit is refused: a converted one would cut or free another part."""
     if isinstance(xs, (list, tuple)):
         try:
             a = array.array("i", xs)
             return a.buffer_info()[0], len(a), a
-        except TypeError:  # elements that are no integers: numpy decides
+        except (TypeError, OverflowError):  # nested lists or no integers: numpy tells them apart
             pass
-    a = np.ascontiguousarray(np.asarray(xs, dtype=np.int32)).reshape(-1)
+    a = np.asarray(xs)
+    if a.size and (a.dtype.kind not in "iu" or a.max() > 2 ** 31 - 1 or a.min() < -2 ** 31):
+        raise ValueError(f"{xs!r} must hold whole numbers that fit int32")
+    a = np.ascontiguousarray(a, dtype=np.int32).reshape(-1)
     return a.ctypes.data, a.size, a
 
 
