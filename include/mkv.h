@@ -380,8 +380,10 @@ MKV_API int mkv_rope(mkv_pool_t pool, int64_t rows, const int32_t* positions, in
  *   k, v device bf16, rows of [Hkv][D], k_stride and v_stride elements from row to row
  *   out  device bf16 [sum(n_tokens)][num_q_heads][D]; rows beyond are left as they were
  * Strides are multiples of 8 elements and at least a row, pointers 16-byte aligned, out overlaps
- * no input.  A masked key or value never reaches an output, also where it is infinite or NaN;
- * visible ones propagate as in the formula.  Sums and the softmax are fp32; the probabilities are
+ * no input.  A masked key or value never reaches an output, also where it is infinite or NaN.
+ * Visible ones do: a score of +inf or NaN makes its row NaN (a row of -inf alone too), and a
+ * non-finite element of v makes its channel of every row that sees it non-finite, infinite or NaN
+ * (where its weight rounds to 0, either may come out).  Sums and the softmax are fp32; the probabilities are
  * rounded to bf16 before they multiply v, the result once more; values of v beyond 2^96 may overflow
  * the fp32 sums, scores that sm_scale makes larger than 2^30 their row's softmax.  Needs no
  * workspace and keeps no state: calls may overlap on different streams and may be captured.

@@ -20,7 +20,10 @@
 //                  tensor memory)
 //   guard          on V chunks that the causal line or the prompt's end crosses: zeroes V rows past
 //                  the end and replaces non-finite V elements by zero, because 0 x inf would reach
-//                  rows that do not see them; the rows that do see them get them back at the end
+//                  rows that do not see them; the rows that do see them get them back at the end,
+//                  added as they are: a weight that underflowed gives an infinity here, and NaN in
+//                  a chunk that went to the tensor core as it was (0 x inf), so the contract says no
+//                  more than that such a channel is non-finite
 //
 // Tensor memory (512 columns): NT x SB score buffers of KT fp32 columns, whose first half the bf16
 // probabilities overwrite, then NT outputs of D columns.
