@@ -4,9 +4,11 @@
 // neighbouring pairs, (x[2i], x[2i + 1]) by the angle pos[axis(i)][row] * inv_freq[i]:
 //   a' = a cos - b sin,  b' = b cos + a sin;  channels from R on are passed through.
 //
-// The angle is formed in fp64 (a position up to 2^31 times an fp32 frequency is exact to 2^-53, so
-// it is known to about 1e-7 rad at any position), reduced to a fraction of a turn and only then
-// rounded to fp32 for the sine and cosine.  The rotation itself is fp32, rounded once to bf16.
+// The angle is formed in fp64, as turns: position times frequency, times 1 / (2 pi), three roundings in
+// all (two products and the constant), so it is off by at most 3 2^-53 of itself: 7e-7 rad at position
+// 2^31 and frequency 1, where one fp32 rounding of the angle would be off by up to 64 rad.  It is reduced to a
+// fraction of a turn and only then rounded to fp32 for the sine and cosine.  The rotation itself is
+// fp32, rounded once to bf16.
 //
 // Bound by memory: q and k are read and written once.  A CTA takes a few rows: its threads first
 // load their vectors, then compute the rows' sines and cosines into shared memory (each angle once
