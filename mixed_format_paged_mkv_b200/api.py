@@ -151,13 +151,14 @@ def _rows_ptr(t, heads, dim, name, device):
     return t.data_ptr(), stride[0] if shape[0] > 1 else heads * dim, shape[0]
 
 
-def _empty_like(t, shape, stream):
-    """A new tensor of t's type and device, from the memory of the stream that will write it."""
+def _empty(shape, dtype, device, stream):
+    """A new tensor from the memory of the stream that will write it: memory of another stream could be
+    given out there again, or still be in use there, while this one's kernels work on it."""
     import torch
     if stream is None:
-        return t.new_empty(shape)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return t.new_empty(shape)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _i32_list(xs):
@@ -271,7 +272,7 @@ class Pool:
         import torch
         if tuple(a.shape) != (128, 256) or tuple(q.shape) != (8, 256):
             raise ValueError("a must be [128, 256] and q [8, 256]")
-        d = torch.empty((128, 8), dtype=torch.float32, device=a.device)
+        d = _empty((128, 8), torch.float32, a.device, stream)
         dev = self.device_index
         _check(lib().mkv_selftest_tc_logits(self.handle, _dev_ptr(a, torch.float16, "a", dev),
                                             _dev_ptr(q, torch.float16, "q", dev),
@@ -320,11 +321,10 @@ class Pool:
             raise ValueError("q must be [len(seq_ids), q_len, Hq, head_dim]")
         qp = _dev_ptr(q, torch.bfloat16, "q", self.device_index)
         if out is None:
-            out = torch.empty((n, q_len, Hq, D), dtype=torch.float32, device=q.device)
+            out = _empty((n, q_len, Hq, D), torch.float32, q.device, stream)
         op = _dev_ptr(out, torch.float32, "out", self.device_index)
         if workspace is None:   # the library checks a caller-given workspace's size itself
-            workspace = torch.empty(self.workspace_bytes(s, q_len, Hq), dtype=torch.uint8,
-                                    device=q.device)
+            workspace = _empty(self.workspace_bytes(s, q_len, Hq), torch.uint8, q.device, stream)
         wp = _dev_ptr(workspace, torch.uint8, "workspace", self.device_index)
         scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
         _check(lib().mkv_decode_attention(self.handle, sp, s.size, q_len, qp, Hq,
@@ -357,12 +357,12 @@ class Pool:
         qp, qs, rows = _rows_ptr(q, Hq, D, "q", dev)
         kp, ks, k_rows = _rows_ptr(k, Hkv, D, "k", dev)
         if q_out is None:
-            q_out = _empty_like(q, (rows, Hq, D), stream)
+            q_out = _empty((rows, Hq, D), q.dtype, q.device, stream)
             qo, qos, q_rows = q_out.data_ptr(), Hq * D, rows
         else:
             qo, qos, q_rows = _rows_ptr(q_out, Hq, D, "q_out", dev)
         if k_out is None:
-            k_out = _empty_like(k, (rows, Hkv, D), stream)
+            k_out = _empty((rows, Hkv, D), k.dtype, k.device, stream)
             ko, kos, o_rows = k_out.data_ptr(), Hkv * D, rows
         else:
             ko, kos, o_rows = _rows_ptr(k_out, Hkv, D, "k_out", dev)
@@ -402,7 +402,7 @@ class Pool:
         if q_rows < rows or k_rows < rows or v_rows < rows:
             raise ValueError(f"q, k and v must have the {rows} rows of n_tokens")
         if out is None:
-            out = _empty_like(q, (q_rows, Hq, D), stream)
+            out = _empty((q_rows, Hq, D), q.dtype, q.device, stream)
             op = out.data_ptr()
         else:
             op, _, o_rows = _rows_ptr(out, Hq, D, "out", dev)
@@ -465,8 +465,8 @@ class Pool:
         _, ctx = self.block_table(seq)
         dev = self.buffers[0].device
         shape = (ctx, self.Hkv, self.D)
-        k_out = torch.empty(shape, dtype=torch.float32, device=dev) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=torch.float32, device=dev) if v_out is None else v_out
+        k_out = _empty(shape, torch.float32, dev, stream) if k_out is None else k_out
+        v_out = _empty(shape, torch.float32, dev, stream) if v_out is None else v_out
         kp = _dev_ptr(k_out, torch.float32, "k_out", self.device_index)
         vp = _dev_ptr(v_out, torch.float32, "v_out", self.device_index)
         cap = min(k_out.numel(), v_out.numel()) // (self.Hkv * self.D)
