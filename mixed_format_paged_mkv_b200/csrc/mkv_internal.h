@@ -111,9 +111,11 @@ struct RowMove {
   int32_t count;
 };
 constexpr int kPageMoveMax = 850, kRowMoveMax = 960;
-// (A launch's cost grows with its parameters: 30 KB take several microseconds, so that short lists go
-// in a smaller block.)
-constexpr int kPageMoveFew = 80, kRowMoveFew = 80;
+// A launch's cost grows with its parameters, so a short call goes in a block of 4 KB: 111 runs of each
+// kind.  Measured, fork + truncate + free of n branches, host time of the three launches: 15 us with 4 KB
+// and 25 to 27 with 30 KB for n = 4, 28 and 40 for n = 81, 34 and 45 for n = 111; blocks of 9 KB cost 1 us
+// a launch more than 4 KB, 3 KB no less.
+constexpr int kMoveFew = 111;
 template <int PAGES, int ROWS>
 struct PageOpLists {
   uint8_t* fp8_slab;
@@ -128,6 +130,8 @@ struct PageOpLists {
   RowMove row[ROWS];
 };
 using PageOpParams = PageOpLists<kPageMoveMax, kRowMoveMax>;
+using PageOpFewParams = PageOpLists<kMoveFew, kMoveFew>;
+static_assert(sizeof(PageOpFewParams) <= 4096, "the block of short calls");
 
 // ------------------------------------------------------------------ materialise (debug / QC)
 // Dense fp32 copy of one sequence's dequantised K and V; never used by decode.

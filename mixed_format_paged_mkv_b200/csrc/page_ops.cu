@@ -94,10 +94,9 @@ cudaError_t launch_page_ops(PageOpParams& p, cudaStream_t s) {
   const int64_t slot = p.fp8_slot_bytes > p.tq3_slot_bytes ? p.fp8_slot_bytes : p.tq3_slot_bytes;
   p.pieces = static_cast<int32_t>((slot + kPieceBytes - 1) / kPieceBytes);
   const unsigned grid = static_cast<unsigned>(p.pages * p.pieces + p.n_row);
-  using Few = PageOpLists<kPageMoveFew, kRowMoveFew>;
-  if (p.n_page <= kPageMoveFew && p.n_row <= kRowMoveFew) {
-    Few f;
-    std::memcpy(&f, &p, offsetof(Few, page));
+  if (p.n_page <= kMoveFew && p.n_row <= kMoveFew) {
+    PageOpFewParams f;
+    std::memcpy(&f, &p, offsetof(PageOpFewParams, page));
     std::memcpy(f.page, p.page, p.n_page * sizeof(PageMove));
     std::memcpy(f.row, p.row, p.n_row * sizeof(RowMove));
     page_ops_kernel<<<grid, kThreads, 0, s>>>(f);
