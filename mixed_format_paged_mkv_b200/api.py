@@ -151,14 +151,15 @@ def _rows_ptr(t, heads, dim, name, device):
     return t.data_ptr(), stride[0] if shape[0] > 1 else heads * dim, shape[0]
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor from the memory of the stream that will write it: memory of another stream could be
-    given out there again, or still be in use there, while this one's kernels work on it."""
+def _empty_like(t, shape, stream, dtype=None):
+    """A new tensor of t's device (and type) from the memory of the stream that will write it: memory of
+    another stream could be given out there again, or still be in use there, while this one's kernels
+    work on it."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return t.new_empty(shape) if dtype is None else t.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return t.new_empty(shape, dtype=dtype or t.dtype)
 
 
 def _i32_list(xs):
@@ -272,7 +273,7 @@ class Pool:
         import torch
         if tuple(a.shape) != (128, 256) or tuple(q.shape) != (8, 256):
             raise ValueError("a must be [128, 256] and q [8, 256]")
-        d = _empty((128, 8), torch.float32, a.device, stream)
+        d = _empty_like(a, (128, 8), stream, torch.float32)
         dev = self.device_index
         _check(lib().mkv_selftest_tc_logits(self.handle, _dev_ptr(a, torch.float16, "a", dev),
                                             _dev_ptr(q, torch.float16, "q", dev),
@@ -321,10 +322,10 @@ class Pool:
             raise ValueError("q must be [len(seq_ids), q_len, Hq, head_dim]")
         qp = _dev_ptr(q, torch.bfloat16, "q", self.device_index)
         if out is None:
-            out = _empty((n, q_len, Hq, D), torch.float32, q.device, stream)
+            out = _empty_like(q, (n, q_len, Hq, D), stream, torch.float32)
         op = _dev_ptr(out, torch.float32, "out", self.device_index)
         if workspace is None:   # the library checks a caller-given workspace's size itself
-            workspace = _empty(self.workspace_bytes(s, q_len, Hq), torch.uint8, q.device, stream)
+            workspace = _empty_like(q, (self.workspace_bytes(s, q_len, Hq),), stream, torch.uint8)
         wp = _dev_ptr(workspace, torch.uint8, "workspace", self.device_index)
         scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
         _check(lib().mkv_decode_attention(self.handle, sp, s.size, q_len, qp, Hq,
@@ -357,12 +358,12 @@ class Pool:
         qp, qs, rows = _rows_ptr(q, Hq, D, "q", dev)
         kp, ks, k_rows = _rows_ptr(k, Hkv, D, "k", dev)
         if q_out is None:
-            q_out = _empty((rows, Hq, D), q.dtype, q.device, stream)
+            q_out = _empty_like(q, (rows, Hq, D), stream)
             qo, qos, q_rows = q_out.data_ptr(), Hq * D, rows
         else:
             qo, qos, q_rows = _rows_ptr(q_out, Hq, D, "q_out", dev)
         if k_out is None:
-            k_out = _empty((rows, Hkv, D), k.dtype, k.device, stream)
+            k_out = _empty_like(k, (rows, Hkv, D), stream)
             ko, kos, o_rows = k_out.data_ptr(), Hkv * D, rows
         else:
             ko, kos, o_rows = _rows_ptr(k_out, Hkv, D, "k_out", dev)
@@ -402,7 +403,7 @@ class Pool:
         if q_rows < rows or k_rows < rows or v_rows < rows:
             raise ValueError(f"q, k and v must have the {rows} rows of n_tokens")
         if out is None:
-            out = _empty((q_rows, Hq, D), q.dtype, q.device, stream)
+            out = _empty_like(q, (q_rows, Hq, D), stream)
             op = out.data_ptr()
         else:
             op, _, o_rows = _rows_ptr(out, Hq, D, "out", dev)
@@ -463,10 +464,9 @@ class Pool:
                    "mkv_materialise_kv")
         import torch
         _, ctx = self.block_table(seq)
-        dev = self.buffers[0].device
         shape = (ctx, self.Hkv, self.D)
-        k_out = _empty(shape, torch.float32, dev, stream) if k_out is None else k_out
-        v_out = _empty(shape, torch.float32, dev, stream) if v_out is None else v_out
+        k_out = _empty_like(self.buffers[0], shape, stream, torch.float32) if k_out is None else k_out
+        v_out = _empty_like(self.buffers[0], shape, stream, torch.float32) if v_out is None else v_out
         kp = _dev_ptr(k_out, torch.float32, "k_out", self.device_index)
         vp = _dev_ptr(v_out, torch.float32, "v_out", self.device_index)
         cap = min(k_out.numel(), v_out.numel()) // (self.Hkv * self.D)
