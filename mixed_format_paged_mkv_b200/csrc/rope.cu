@@ -25,6 +25,7 @@ namespace mkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kSms = 148;
 
 __device__ __forceinline__ void sincos_turns(int32_t pos, float inv_freq, float* s, float* c) {
   constexpr double kInvTwoPi = 0.15915494309189533577;
@@ -158,10 +159,13 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
 cudaError_t launch_rope(RopeParams& p, cudaStream_t s) {
   if (p.rows <= 0) return cudaSuccess;
   const int64_t heads = p.Hq + p.Hkv, per_row = heads * (p.vec ? p.D / 16 : p.D / 2);
-  // rows of a CTA: kUnits units a thread, but no fewer CTAs than give every SM two (a decode step's few
-  // rows: measured 64 rows of 40 heads, D 128)
+  // Rows of a CTA: kUnits units a thread, but no fewer CTAs than two for each of the 148 SMs where there
+  // are as many rows: the few rows of a decode step wait for one CTA's chain of loads, angles and stores.
+  // Device time in us without that limit, with one, two and four CTAs per SM: 64 rows of 32/8 heads, D 128:
+  // 2.9, 2.3, 2.3, 2.3; 900 rows of 16/4, D 64: 3.4, 2.9, 2.7, 4.6; 600 rows of 32/8, D 128: 4.0, 4.0, 3.8,
+  // 4.8; 444 rows of 24/4, D 256: 4.0, 4.0, 3.5, 3.4; from 4000 rows on within 2% of one another.
   int64_t r = std::max<int64_t>(1, kUnits * kThreads / per_row);
-  r = std::min<int64_t>({r, 64, std::max<int64_t>(1, p.rows / 296)});
+  r = std::min<int64_t>({r, 64, std::max<int64_t>(1, p.rows / (2 * kSms))});
   p.cta_rows = static_cast<int32_t>(r);
   // i / heads for the units of a CTA (i < 2^32 / heads; at least two heads, one of q and one of k)
   p.heads_magic = static_cast<uint32_t>((1ull << 32) / heads + 1);
