@@ -40,7 +40,8 @@
  * Ownership: every device buffer is allocated and owned by the caller (e.g. by PyTorch) and
  * must outlive the pool; the pool owns only host state (allocators, the host copy of the
  * tables, protection flags).  Every call works on the device of the pool's buffers, whichever is
- * current, and leaves the current one as it was.  All device work is asynchronous on the caller's
+ * current, and leaves the current one as it was (the decode kernels are set up for the first device
+ * that a process decodes on: one process per GPU).  All device work is asynchronous on the caller's
  * stream (a cudaStream_t of that device passed as void*; NULL = its legacy default stream); inputs
  * and outputs lie on that device and must stay valid until the stream reaches the call.  Calls on one pool must come from one host thread at a time and
  * be ordered on one stream (or ordered by the caller): slots freed by a call are reused by
@@ -285,7 +286,9 @@ MKV_API int mkv_seq_fork(mkv_pool_t pool, const int32_t* src_ids, const int32_t*
 
 /* Roll sequences back to their first n_tokens[i] tokens (rejected speculative tokens): pages past
  * the new end are given up, rows past it in its page become zero (the page's scales stay), after
- * the page was copied to a slot of the sequence's own where others share it.  Slots are taken in
+ * the page was copied to a slot of the sequence's own where others share it.  A dropped token that
+ * had widened its page's scale leaves it wide: the rows before it were re-encoded when it was
+ * appended, and rows appended later are encoded with that scale or a larger one.  Slots are taken in
  * list order before any is freed.  A call split over several launches (more than 850 new ends
  * inside a page, or more than 960 sequences that give up pages) takes effect launch by launch in
  * list order, so one that fails has rolled back a leading part of the list.  Errors: BAD_SEQ, INVALID_ARG (also n_tokens[i] above the length), UNSUPPORTED
@@ -356,7 +359,8 @@ MKV_API int mkv_prefill_kv(mkv_pool_t pool, const int32_t* seq_ids, const int32_
  * where (a, b) are the channels (i, i + n_freq), or (2i, 2i + 1) when interleaved != 0.  Channels
  * from 2 * n_freq on are copied.  The pool gives Hkv and D.
  *   positions  device int32 [n_axes][rows]      inv_freq  device fp32 [n_freq], n_freq <= D / 2
- *   axis_of    host [n_freq], each in [0, n_axes); NULL: axis 0 (n_axes <= 128)
+ *   axis_of    host [n_freq], each in [0, n_axes); NULL: axis 0 for all, the other axes'
+ *              positions are then not read (n_axes <= 128)
  *   q_in/q_out device bf16, rows of [num_q_heads][D], strides in elements; q_out may be q_in
  *   k_in/k_out the same with Hkv heads
  * An output overlaps no other array, but parts of one fused array may be rotated in place.  Any
@@ -388,7 +392,9 @@ MKV_API int mkv_rope(mkv_pool_t pool, int64_t rows, const int32_t* positions, in
  * rounded to bf16 before they multiply v, the result once more; values of v beyond 2^96 may overflow
  * the fp32 sums, scores that sm_scale makes larger than 2^30 their row's softmax.  Needs no
  * workspace and keeps no state: calls may overlap on different streams and may be captured.
- * Errors: INVALID_ARG (also sm_scale outside [0, 65536]), UNSUPPORTED (g > 128), CUDA. */
+ * Errors: INVALID_ARG (also sm_scale outside [0, 65536]: a row's reference follows its largest
+ * q . k, which has the largest weight only where the scale is not negative), UNSUPPORTED (g > 128),
+ * CUDA. */
 MKV_API int mkv_prompt_attention(mkv_pool_t pool, const int32_t* n_tokens, int32_t n_prompts,
                                  const void* q_bf16, int64_t q_stride, const void* k_bf16,
                                  int64_t k_stride, const void* v_bf16, int64_t v_stride,

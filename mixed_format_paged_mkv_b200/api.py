@@ -346,7 +346,7 @@ class Pool:
              stream=None):
         """Rotate q bf16 [rows, Hq, D] and k bf16 [rows, Hkv, D] (rows may be strided) by
         ``positions`` (int32 [rows] or [n_axes, rows]) times ``inv_freq`` (fp32 [n_freq]); ``axes``
-        lists the axis of each frequency (default: axis 0).  Pairs are channels n_freq apart, or
+        lists the axis of each frequency (default: axis 0 for all of them).  Pairs are channels n_freq apart, or
         neighbours when ``interleaved``.  Returns (q_out, k_out): new tensors unless given; the
         inputs themselves for a rotation in place (mkv_rope)."""
         import torch

@@ -9,8 +9,12 @@
 // share the KV head, token-major, so K and V are read once for all of them and only the keys up to
 // the tile's last token are visited.  An item is NT tiles of consecutive tokens (D 64 and 128: two,
 // which share K and V; D 256: one, whose output takes half of tensor memory).  A CTA (one per SM)
-// works on items until none is left; it gets the next one by cluster launch control, so items go to
-// whichever SM is free, the ones with most keys first.
+// works on items until none is left; it gets the next one by cluster launch control.  Items go out
+// prompt by prompt, the longest first, and within a prompt those with most keys first.  A CTA claims an
+// item when it starts the one before, so that the loads of the next are never waited for; the claim
+// therefore does not know how long the present item takes, which shows where an SM gets few items: one
+// prompt of 2048 tokens, 32/8 heads, D 128 (1.7 items per SM) takes 50 us where free SMs taking the
+// items would need 37.
 //
 // Roles:
 //   softmax warps  4 per tile, one row per thread: scores from tensor memory, probabilities back
@@ -33,8 +37,10 @@
 // The reference m moves only when a row's maximum exceeds it by more than 8 in log2 units, so
 // p <= 2^8 and the sums stay far inside fp32; each move rescales the fp32 output.
 //
-// Measured (one B200, one prompt of 8192 tokens, causal FLOPs): 32/8 heads, D 128: 440 us, 1250
-// TFLOP/s; 24/4 heads, D 256: 655 us, 1260 TFLOP/s; 16/16 heads, D 64: 199 us, 690 TFLOP/s.
+// Measured (one B200, one prompt of 8192 tokens, causal FLOPs; from a cool card to one at its power
+// limit): 32/8 heads, D 128: 440-460 us, 1250-1200 TFLOP/s; 24/4 heads, D 256: 655-772 us, 1260-1070
+// TFLOP/s; 16/16 heads, D 64: 199 us, 690 TFLOP/s.  Device time at D 128, 32/8 heads over prompts of 64 to
+// 4096 tokens: 3.6 us + 0.9 us a step + 4.1 us an item (of each SM's share), and the claim's imbalance.
 //   D 128: scores of 64 keys take 48 cycles per MMA instead of 32, since each reads 6 KB of operands
 //          from shared memory; with the products and the softmax's share of tensor memory the tensor
 //          path needs about 1600 of the 1740 cycles of a step.  Steps of 128 keys read less but leave
