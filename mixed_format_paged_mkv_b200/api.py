@@ -151,15 +151,19 @@ def _rows_ptr(t, heads, dim, name, device):
     return t.data_ptr(), stride[0] if shape[0] > 1 else heads * dim, shape[0]
 
 
-def _empty_like(t, shape, stream, dtype=None):
+def _empty_like(t, shape, stream, dtype=None, returned=True):
     """A new tensor of t's device (and type) from the memory of the stream that will write it: memory of
     another stream could be given out there again, or still be in use there, while this one's kernels
-    work on it."""
+    work on it.  What the caller gets is also held for the caller's current stream, which usually reads
+    it: given up, its memory waits for both."""
     import torch
     if stream is None:
         return t.new_empty(shape) if dtype is None else t.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return t.new_empty(shape, dtype=dtype or t.dtype)
+        new = t.new_empty(shape, dtype=dtype or t.dtype)
+    if returned:
+        new.record_stream(torch.cuda.current_stream(t.device))
+    return new
 
 
 def _i32_list(xs):
@@ -325,7 +329,7 @@ class Pool:
             out = _empty_like(q, (n, q_len, Hq, D), stream, torch.float32)
         op = _dev_ptr(out, torch.float32, "out", self.device_index)
         if workspace is None:   # the library checks a caller-given workspace's size itself
-            workspace = _empty_like(q, (self.workspace_bytes(s, q_len, Hq),), stream, torch.uint8)
+            workspace = _empty_like(q, (self.workspace_bytes(s, q_len, Hq),), stream, torch.uint8, returned=False)
         wp = _dev_ptr(workspace, torch.uint8, "workspace", self.device_index)
         scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
         _check(lib().mkv_decode_attention(self.handle, sp, s.size, q_len, qp, Hq,

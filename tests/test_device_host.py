@@ -46,7 +46,7 @@ def q(n, heads=4):
 
 def decode(p, **kw):
     ws = torch.zeros(p.workspace_bytes([0], 1, 4) + 256, dtype=torch.uint8)
-    p.decode([0], q(1), workspace=ws[-ws.data_ptr() % 256:], **kw)
+    p.decode([0], q(1), out=torch.zeros((1, 1, 4, 64)), workspace=ws[-ws.data_ptr() % 256:], **kw)
 
 
 def noalloc(p):
